@@ -468,11 +468,136 @@ mlstm_status_t mlstm_step(const mlstm_step_params_t* p,
                           float* C, float* n, float* m, void* h,
                           mlstm_stream_t stream);
 
+/*
+ * The gated delta rule with one decay and one write strength per head and token (the reduction of
+ * Gated DeltaNet-2 that burn-gdn2 config.rs names: b = w = beta 1 and a scalar decay), for
+ * prefill, decoding and training.  Per sequence and value head, state S [K, V] fp32, for each
+ * token t:
+ *     S' = exp(g_t) S;   r = S'^T k_t;   S = S' + beta_t k_t (v_t - r)^T;   o_t = S^T q_t
+ * Value head h reads q and k of head h / (H / HK).  Scaling of q and normalisation of k are the
+ * caller's.
+ *
+ * Strides.  q, k, v, g, beta, o (and the gradients' tensors) are indexed [batch, head, token] by
+ * the strides given here, in elements; the last axis of q, k, v, o is contiguous.  So a projection's
+ * output [B,T,heads,width], or a slice of a wider one, is read where it lies.  Strides are >= 0 (0
+ * repeats an input); those of q, k, v, o are multiples of 16 bytes, and distinct elements of an
+ * output lie apart.  States are dense.
+ *
+ * Packed sequences (num_seqs = N > 0).  B is 1 and sequence n is the tokens seq_offsets[n] ..
+ * seq_offsets[n+1] - 1 of the T tokens: seq_offsets [N+1] int32 on the device, not decreasing, at most
+ * T.  A sequence may be empty: its final state is its initial state.  Tokens that no sequence holds
+ * are neither read nor written.  (Offsets out of this order are bounded on the device: no access
+ * leaves the tensors, but which tokens a sequence then takes is unspecified.)  num_seqs = 0: each
+ * batch row is one sequence of T tokens, N = B.
+ *
+ *   p->mode  MLSTM_GDR_RECURRENT: token by token, fp32 arithmetic; K a multiple of 8, at most 256.
+ *            MLSTM_GDR_CHUNK: chunks of 64 tokens on the tensor cores, a triangular solve per chunk;
+ *            K a multiple of 8, at most 128.  Operands are split into 16-bit parts so that states and
+ *            gate gradients keep fp32 accuracy.
+ *            MLSTM_GDR_AUTO: CHUNK from 32 tokens (T) on where K allows it, else RECURRENT.
+ *   V        a multiple of 8
+ *   q, k     [B,HK,T,K]  dtype      required (if B, T > 0)
+ *   v, o     [B,H,T,V]   dtype      required; o must not overlap an input
+ *   g        [B,H,T]     fp32       log decay, <= 0 for a decay; -infinity forgets the state
+ *   beta     [B,H,T]     fp32       write strength (0 .. 1, or .. 2)
+ *   S0       [N,H,K,V]   fp32       initial states; NULL = zeros
+ *   S_out    [N,H,K,V]   fp32       final states; NULL = not written; may equal S0 exactly
+ *   workspace, workspace_bytes      at least mlstm_gdr_fwd_workspace_size(p) bytes (0 for RECURRENT),
+ *                                   16-byte aligned; contents are garbage before and after.  Two calls
+ *                                   in flight must not share it.
+ *
+ * mlstm_gdr_step: one token for each of B rows, states updated in place.  q, k [B,HK,K], v, o [B,H,V],
+ * g, beta [B,H] by the strides in p (t is ignored).  S [pool,H,K,V] fp32 dense.  slots [B] int32
+ * (device): row b's state is S[slots[b]]; a slot outside 0 .. pool - 1 marks a padding row (o = 0, no
+ * state is touched); rows with the same slot are taken in the batch's order.  slots NULL: row b has
+ * S[b], and pool >= B.  K a multiple of 8, at most 256; V a multiple of 8.
+ *
+ * mlstm_gdr_bwd: gradients of a loss given dout = dL/do [B,H,T,V] (dtype, strides p->o) and
+ * dS = dL/dS_out [N,H,K,V] fp32 (NULL = 0).  dq, dk [B,HK,T,K] and dv [B,H,T,V] in the inputs' dtype
+ * (each rounded once from fp32) by the strides s_dq, s_dk, s_dv; dg, dbeta [B,H,T] fp32 dense; dS0
+ * [N,H,K,V] fp32.  All but dS0 (NULL = not written) are required if B, T > 0; gradients of q and k are
+ * summed over the value heads that share them.  p->mode is ignored; K a multiple of 8, at most 128.
+ * Sums have a fixed order: the same call gives the same bits.
+ */
+typedef enum { MLSTM_GDR_AUTO = 0, MLSTM_GDR_RECURRENT = 1, MLSTM_GDR_CHUNK = 2 } mlstm_gdr_mode_t;
+typedef struct {
+  long long b, h, t; /* elements between batch rows, heads and tokens */
+} mlstm_gdr_stride_t;
+typedef struct {
+  int B, HK, H, T, K, V;
+  int num_seqs;
+  mlstm_dtype_t dtype;
+  int mode; /* mlstm_gdr_mode_t */
+  mlstm_gdr_stride_t q, k, v, g, beta, o;
+} mlstm_gdr_params_t;
+typedef struct {
+  int B, HK, H, K, V;
+  int pool;
+  mlstm_dtype_t dtype;
+  mlstm_gdr_stride_t q, k, v, g, beta, o;
+} mlstm_gdr_step_params_t;
+size_t mlstm_gdr_fwd_workspace_size(const mlstm_gdr_params_t* p);
+mlstm_status_t mlstm_gdr_fwd(const mlstm_gdr_params_t* p, const void* q, const void* k, const void* v, const float* g,
+                             const float* beta, const float* S0, const int* seq_offsets, void* o, float* S_out,
+                             void* workspace, size_t workspace_bytes, mlstm_stream_t stream);
+mlstm_status_t mlstm_gdr_step(const mlstm_gdr_step_params_t* p, const void* q, const void* k, const void* v,
+                              const float* g, const float* beta, const int* slots, float* S, void* o,
+                              mlstm_stream_t stream);
+size_t mlstm_gdr_bwd_workspace_size(const mlstm_gdr_params_t* p);
+mlstm_status_t mlstm_gdr_bwd(const mlstm_gdr_params_t* p, const void* q, const void* k, const void* v, const float* g,
+                             const float* beta, const float* S0, const int* seq_offsets, const void* dout,
+                             const float* dS, mlstm_gdr_stride_t s_dq, mlstm_gdr_stride_t s_dk,
+                             mlstm_gdr_stride_t s_dv, void* dq, void* dk, void* dv, float* dg, float* dbeta,
+                             float* dS0, void* workspace, size_t workspace_bytes, mlstm_stream_t stream);
+
+/*
+ * Root-mean-square norm of a residual stream (the pre-norm of the xLSTM 7B block) with the residual's
+ * addition, for the projections that follow it in the storage type or in 8 bits.  Per row of D
+ * channels:
+ *     r = x + residual;   y = r / sqrt(mean(r^2) + eps) * weight
+ * The norm reads the sum before it is rounded to the storage type.
+ *
+ *   p->quant   MLSTM_RMS_NONE: y has the storage type.  MLSTM_RMS_E4M3 (8-bit floating point, largest
+ *              value 448) or MLSTM_RMS_INT8 (-127 .. 127): a group of p->group channels shares the
+ *              fp32 scale max|y| / 448 (or / 127), 1 where the group is zero, and holds y / scale
+ *              rounded to nearest even.  group is 0 (the whole row) or 128 (the last group of a row may
+ *              be shorter).
+ *   x          [rows,D] dtype        required (if rows > 0)
+ *   residual   [rows,D] dtype        NULL = 0
+ *   weight     [D] fp32              NULL = 1
+ *   r_out      [rows,D] dtype        the sum; required with residual, else ignored; may equal residual
+ *                                    or x exactly (in place)
+ *   y          [rows,D] dtype or 8 bits   must not overlap the others
+ *   scales     [rows, groups] fp32   required with quant, else ignored
+ * D in 1 .. 16384; eps >= 0.
+ *
+ * mlstm_rms_norm_bwd: r [rows,D] is the sum that was normalised (r_out, or x without a residual), dy =
+ * dL/dy, dresidual = dL/dr_out (NULL = 0), all of the storage type.  dx = the gradient of x and of
+ * residual alike, storage type; may equal dy or dresidual exactly.  dweight [D] fp32, NULL = not
+ * wanted; workspace: mlstm_rms_norm_bwd_workspace_size bytes, needed for dweight.  Sums have a fixed
+ * order.  p->quant and p->group are ignored.
+ */
+typedef enum { MLSTM_RMS_NONE = 0, MLSTM_RMS_E4M3 = 1, MLSTM_RMS_INT8 = 2 } mlstm_rms_quant_t;
+typedef struct {
+  long long rows;
+  int D;
+  mlstm_dtype_t dtype;
+  int quant; /* mlstm_rms_quant_t */
+  int group;
+  float eps;
+} mlstm_rms_params_t;
+mlstm_status_t mlstm_rms_norm(const mlstm_rms_params_t* p, const void* x, const void* residual, const float* weight,
+                              void* r_out, void* y, float* scales, mlstm_stream_t stream);
+size_t mlstm_rms_norm_bwd_workspace_size(const mlstm_rms_params_t* p);
+mlstm_status_t mlstm_rms_norm_bwd(const mlstm_rms_params_t* p, const void* dy, const void* r, const float* weight,
+                                  const void* dresidual, void* dx, float* dweight, void* workspace,
+                                  size_t workspace_bytes, mlstm_stream_t stream);
+
 /* Static, never-NULL description of a status code. */
 const char* mlstm_status_string(mlstm_status_t s);
 
 /* ABI version: (major << 16) | minor.  2.3: mlstm_bwd needs its workspace whenever
- * mlstm_bwd_workspace_size is nonzero, an empty sequence included. */
+ * mlstm_bwd_workspace_size is nonzero, an empty sequence included.  2.4: mlstm_gdr_*, mlstm_rms_*. */
 int mlstm_abi_version(void);
 
 #ifdef __cplusplus

@@ -127,4 +127,60 @@ size_t bwd_workspace_bytes(long long BH, int S, int nb);
 bool bwd_supported(int dk, int dv, int dtype);
 cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t stream);
 
+// Root-mean-square norm (rms_norm.cu) and its gradients.  x, res, r_out, y [rows, D] dtype (y 8 bits
+// when kind is 1 (e4m3) or 2 (int8)); gradients: x = the normalised sum, res = its own gradient
+// (may be NULL), y = dx, part = the workspace.
+struct RmsArgs {
+  long long rows;
+  int D, dtype, kind, group;  // group: channels to a scale, D = one scale a row
+  float eps;
+  const void *x, *res, *dy;
+  const float* weight;
+  void *r_out, *y;
+  float *scales, *dweight, *part;
+};
+bool rms_norm_supported(int D);
+size_t rms_norm_bwd_workspace_bytes(long long rows, int D);
+cudaError_t launch_rms_norm(const RmsArgs& a, cudaStream_t stream);
+cudaError_t launch_rms_norm_bwd(const RmsArgs& a, cudaStream_t stream);
+
+// Gated delta rule (gdr.cu, gdr_chunk.cu, gdr_bwd.cu).  N sequences: sequence n is batch row n, or,
+// with offsets, the tokens offsets[n] .. offsets[n + 1] of batch row 0.  Strides in elements.
+struct GdrStride {
+  long long b, h, t;
+};
+struct GdrArgs {
+  int N, HK, H, T, K, V, dtype;
+  const int* offsets;  // [N + 1] or NULL
+  const void *q, *k, *v;
+  const float *g, *beta, *S0;
+  void* o;
+  float* S_out;
+  GdrStride sq, sk, sv, sg, sb, so;
+  // gradients (gdr_bwd.cu)
+  const void* dout;
+  const float* dS;
+  void *dq, *dk, *dv;
+  GdrStride sdq, sdk, sdv;
+  float *dg, *dbeta, *dS0;
+};
+cudaError_t launch_gdr_recurrent(const GdrArgs& a, cudaStream_t stream);
+// chunks of 64 tokens on the tensor cores (gdr_chunk.cu)
+constexpr int kGdrChunkFrom = 32;
+bool gdr_chunk_supported(int K);
+size_t gdr_chunk_workspace_bytes(const GdrArgs& a);
+cudaError_t launch_gdr_chunk(const GdrArgs& a, void* ws, cudaStream_t stream);
+
+// One token for each of B rows; row b's state is S[slots[b]] of `pool` states (slots NULL: S[b]).
+struct GdrStepArgs {
+  int B, HK, H, K, V, dtype, pool;
+  const void *q, *k, *v;
+  const float *g, *beta;
+  const int* slots;
+  float* S;
+  void* o;
+  GdrStride sq, sk, sv, sg, sb, so;
+};
+cudaError_t launch_gdr_step(const GdrStepArgs& a, cudaStream_t stream);
+
 }  // namespace mlstm

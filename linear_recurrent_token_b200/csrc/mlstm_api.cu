@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include "bounds.cuh"
+#include "host_check.h"
 #include "kernels.h"
 #include "mlstm.h"
 
@@ -89,18 +90,6 @@ WsLayout fwd_layout(const FwdShape& s, bool scalar_n = false) {
   off = align_up(off + sizeof(float) * (size_t)s.BH * s.nb * s.dk);
   w.total = off;
   return w;
-}
-
-bool misaligned(const void* p) { return ((uintptr_t)p & 15) != 0; }
-
-struct Range {
-  const void* p;
-  size_t n;
-};
-bool overlaps(Range a, Range b) {
-  if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
-  const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-  return a0 < b0 + b.n && b0 < a0 + a.n;
 }
 
 // GroupNorm + SiLU gate applied to h after the recurrence: one more kernel over h in place
@@ -317,7 +306,7 @@ mlstm_status_t check_bwd(const mlstm_fwd_params_t* p, FwdShape* s) {
 
 extern "C" {
 
-int mlstm_abi_version(void) { return (2 << 16) | 3; }
+int mlstm_abi_version(void) { return (2 << 16) | 4; }
 
 const char* mlstm_status_string(mlstm_status_t s) {
   switch (s) {

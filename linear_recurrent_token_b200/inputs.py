@@ -168,3 +168,21 @@ def gdn2_inputs(B, H, T, K, V, dtype, seed, with_state=True):
     w = round_to(rng.uniform(0, 1, (B, H, T, V)), "f32")
     S0 = _draw(rng, (B, H, K, V), "f32", scale=0.1) if with_state else None
     return dict(q=q, k=k, v=v, g=g, b=b, w=w, S0=S0)
+
+
+def gdr_inputs(B, HK, H, T, K, V, dtype, seed, with_state=True):
+    """Inputs of a gated delta rule call: q ~ N(0,1)/sqrt(K), v ~ N(0,1), k ~ N(0,1) scaled to unit
+    length per token; log decay g = -exp(pace + N(0, 0.5^2)) with a pace per head from -6.5 (memories of
+    hundreds of tokens) to -1.5 (a few tokens); beta ~ sigmoid(N(0,1)); S0 ~ N(0, 0.1^2).  Dict of float32
+    numpy arrays holding the exact stored values (dtype "f64": unrounded float64)."""
+    rng = np.random.default_rng(seed)
+    keep = (lambda x, d: x) if dtype == "f64" else round_to
+    q = keep(rng.standard_normal((B, HK, T, K)) / np.sqrt(K), dtype)
+    kr = rng.standard_normal((B, HK, T, K))
+    k = keep(kr / np.maximum(np.linalg.norm(kr, axis=-1, keepdims=True), 1e-12), dtype)
+    v = keep(rng.standard_normal((B, H, T, V)), dtype)
+    pace = np.linspace(-6.5, -1.5, H)[None, :, None]
+    g = keep(-np.exp(pace + 0.5 * rng.standard_normal((B, H, T))), "f32")
+    beta = keep(1.0 / (1.0 + np.exp(-rng.standard_normal((B, H, T)))), "f32")
+    S0 = keep(0.1 * rng.standard_normal((B, H, K, V)), "f32") if with_state else None
+    return dict(q=q, k=k, v=v, g=g, beta=beta, S0=S0)

@@ -43,6 +43,32 @@ class Gdn2Params(ctypes.Structure):
 GDN2_RECURRENT, GDN2_CHUNK = 0, 1
 
 
+class GdrStride(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_longlong), ("h", ctypes.c_longlong), ("t", ctypes.c_longlong)]
+
+
+class GdrParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("HK", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int),
+                ("K", ctypes.c_int), ("V", ctypes.c_int), ("num_seqs", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("mode", ctypes.c_int), ("q", GdrStride), ("k", GdrStride), ("v", GdrStride), ("g", GdrStride),
+                ("beta", GdrStride), ("o", GdrStride)]
+
+
+class GdrStepParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("HK", ctypes.c_int), ("H", ctypes.c_int), ("K", ctypes.c_int),
+                ("V", ctypes.c_int), ("pool", ctypes.c_int), ("dtype", ctypes.c_int), ("q", GdrStride),
+                ("k", GdrStride), ("v", GdrStride), ("g", GdrStride), ("beta", GdrStride), ("o", GdrStride)]
+
+
+class RmsParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("quant", ctypes.c_int),
+                ("group", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+GDR_MODES = {"auto": 0, "recurrent": 1, "chunk": 2}
+RMS_QUANT = {None: 0, "e4m3": 1, "int8": 2}
+
+
 class FwdPlan(ctypes.Structure):
     _fields_ = [("tensor_core", ctypes.c_int), ("segments", ctypes.c_int), ("dv_tile", ctypes.c_int),
                 ("ctas_main", ctypes.c_int), ("kernels", ctypes.c_int), ("workspace_bytes", ctypes.c_size_t),
@@ -141,6 +167,22 @@ def _load(path):
     L.mlstm_bwd.restype = I
     L.mlstm_step.argtypes = [ctypes.POINTER(StepParams)] + [P] * 10 + [P]
     L.mlstm_step.restype = I
+    L.mlstm_gdr_fwd_workspace_size.argtypes = [ctypes.POINTER(GdrParams)]
+    L.mlstm_gdr_fwd_workspace_size.restype = Z
+    L.mlstm_gdr_fwd.argtypes = [ctypes.POINTER(GdrParams)] + [P] * 10 + [Z, P]
+    L.mlstm_gdr_fwd.restype = I
+    L.mlstm_gdr_step.argtypes = [ctypes.POINTER(GdrStepParams)] + [P] * 9
+    L.mlstm_gdr_step.restype = I
+    L.mlstm_gdr_bwd_workspace_size.argtypes = [ctypes.POINTER(GdrParams)]
+    L.mlstm_gdr_bwd_workspace_size.restype = Z
+    L.mlstm_gdr_bwd.argtypes = [ctypes.POINTER(GdrParams)] + [P] * 9 + [GdrStride] * 3 + [P] * 7 + [Z, P]
+    L.mlstm_gdr_bwd.restype = I
+    L.mlstm_rms_norm.argtypes = [ctypes.POINTER(RmsParams)] + [P] * 7
+    L.mlstm_rms_norm.restype = I
+    L.mlstm_rms_norm_bwd_workspace_size.argtypes = [ctypes.POINTER(RmsParams)]
+    L.mlstm_rms_norm_bwd_workspace_size.restype = Z
+    L.mlstm_rms_norm_bwd.argtypes = [ctypes.POINTER(RmsParams)] + [P] * 7 + [Z, P]
+    L.mlstm_rms_norm_bwd.restype = I
     L.mlstm_status_string.argtypes = [I]
     L.mlstm_status_string.restype = ctypes.c_char_p
     L.mlstm_abi_version.argtypes = []
@@ -497,3 +539,266 @@ def step(q, k, v, igate, fgate, C, n, m, ogate=None, *, num_blocks: int = 1, ret
     if st != 0:
         raise MlstmError(st, "mlstm_step")
     return h
+
+
+# --------------------------------------------------------------- gated delta rule, root-mean-square norm
+
+def _want(name, t, shape, dtype, device, contiguous=False):
+    """Refuses a tensor of another shape, type, layout or device; None passes."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, q (or x) on {device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _need_cuda(t):
+    if t.device.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, got {t.device}")
+
+
+def _gdr_stride(name, t, last=True) -> GdrStride:
+    """Strides of [batch, head, token(, width)]; those of axes with one element are never used."""
+    if last and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return GdrStride(*(t.stride(i) if i < t.dim() - int(last) and t.shape[i] > 1 else 0 for i in range(3)))
+
+
+@contextlib.contextmanager
+def _on(device, stream, *tensors):
+    """Makes the device and the stream current, so that what is allocated inside belongs to the stream,
+    and tells the allocator of tensors that come from another one."""
+    with torch.cuda.device(device):
+        if stream is None or stream == torch.cuda.current_stream():
+            yield _stream_ptr(stream)
+            return
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            yield _stream_ptr(stream)
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=device) if need else None), need
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _gdr_shapes(q, k, v, g, beta, seq_offsets):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k are [B, HK, T, K] and v is [B, H, T, V]")
+    _dtype_code(q)
+    B, HK, T, K = q.shape
+    H, V = v.shape[1], v.shape[3]
+    _want("k", k, q.shape, q.dtype, q.device)
+    _want("v", v, (B, H, T, V), q.dtype, q.device)
+    _want("g", g, (B, H, T), torch.float32, q.device)
+    _want("beta", beta, (B, H, T), torch.float32, q.device)
+    N = B
+    if seq_offsets is not None:
+        if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2 or B != 1:
+            raise ValueError("seq_offsets is [N + 1] with N >= 1, and packed tensors have one batch row")
+        _want("seq_offsets", seq_offsets, seq_offsets.shape, torch.int32, q.device, contiguous=True)
+        N = seq_offsets.shape[0] - 1
+    return B, HK, H, T, K, V, N
+
+
+def gdr_params(q, k, v, g, beta, o=None, seq_offsets=None, mode: str = "auto") -> GdrParams:
+    """Sizes and strides of a call; o: the output, or the gradient of it (None: dense like v's shape)."""
+    B, HK, H, T, K, V, N = _gdr_shapes(q, k, v, g, beta, seq_offsets)
+    if mode not in GDR_MODES:
+        raise ValueError(f"mode must be one of {tuple(GDR_MODES)}, got {mode!r}")
+    so = GdrStride(H * T * V, T * V, V) if o is None else _gdr_stride("o", o)
+    return GdrParams(B, HK, H, T, K, V, 0 if seq_offsets is None else N, _dtype_code(q), GDR_MODES[mode],
+                     _gdr_stride("q", q), _gdr_stride("k", k), _gdr_stride("v", v), _gdr_stride("g", g, False),
+                     _gdr_stride("beta", beta, False), so)
+
+
+def gdr_fwd_workspace_size(params: GdrParams) -> int:
+    return int(lib().mlstm_gdr_fwd_workspace_size(ctypes.byref(params)))
+
+
+def gdr_bwd_workspace_size(params: GdrParams) -> int:
+    return int(lib().mlstm_gdr_bwd_workspace_size(ctypes.byref(params)))
+
+
+def _like(t, packed):
+    """An output laid out like t where t fills its memory, else dense; zeros where packed sequences may
+    leave tokens out."""
+    return torch.zeros_like(t) if packed else torch.empty_like(t)
+
+
+def gdr_fwd(q, k, v, g, beta, S0=None, *, seq_offsets=None, mode: str = "auto", o=None, S_out=None,
+            return_state: bool = True, workspace=None, stream=None):
+    """The gated delta rule over sequences (mlstm_gdr_fwd): q, k [B,HK,T,K], v [B,H,T,V] (fp32 or bf16,
+    H a multiple of HK); g (log decay), beta [B,H,T] fp32; S0 [N,H,K,V] fp32 or None.  Tensors may be
+    strided views with a contiguous last axis (a projection's [B,T,heads,width], transposed).
+    seq_offsets [N+1] int32 packs N sequences into one batch row; tokens of no sequence stay as they are
+    in a given o and are zero in a new one.  mode "auto", "recurrent" or "chunk".  S_out may be S0.
+    Returns (o, S_out)."""
+    B, HK, H, T, K, V, N = _gdr_shapes(q, k, v, g, beta, seq_offsets)
+    _want("S0", S0, (N, H, K, V), torch.float32, q.device, contiguous=True)
+    _want("S_out", S_out, (N, H, K, V), torch.float32, q.device, contiguous=True)
+    _want("o", o, v.shape, q.dtype, q.device)
+    gdr_params(q, k, v, g, beta, o, seq_offsets, mode)
+    _need_cuda(q)
+    with _on(q.device, stream, q, k, v, g, beta, S0, seq_offsets, o, S_out, workspace) as s:
+        if o is None:
+            o = _like(v, seq_offsets is not None)
+        if return_state and S_out is None:
+            S_out = torch.empty((N, H, K, V), dtype=torch.float32, device=q.device)
+        p = gdr_params(q, k, v, g, beta, o, seq_offsets, mode)
+        workspace, ws_len = _workspace(workspace, gdr_fwd_workspace_size(p), q.device)
+        st = lib().mlstm_gdr_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
+                                 _ptr(seq_offsets), _ptr(o), _ptr(S_out), _ptr(workspace), ctypes.c_size_t(ws_len), s)
+    if st != 0:
+        raise MlstmError(st, "mlstm_gdr_fwd")
+    return o, S_out
+
+
+def gdr_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None):
+    """One token of the gated delta rule for each row (mlstm_gdr_step), states updated in place: q, k
+    [B,HK,K], v [B,H,V], g, beta [B,H] fp32, S [pool,H,K,V] fp32; slots [B] int32 names each row's state
+    (None: row b has S[b]), a slot outside the pool marks padding (its o is zero).  Returns o [B,H,V]."""
+    if q.dim() != 3 or v.dim() != 3 or S.dim() != 4:
+        raise ValueError("q, k are [B, HK, K], v is [B, H, V] and S is [pool, H, K, V]")
+    B, HK, K = q.shape
+    H, V = v.shape[1], v.shape[2]
+    code = _dtype_code(q)
+    _want("k", k, q.shape, q.dtype, q.device)
+    _want("v", v, (B, H, V), q.dtype, q.device)
+    _want("g", g, (B, H), torch.float32, q.device)
+    _want("beta", beta, (B, H), torch.float32, q.device)
+    _want("S", S, (S.shape[0], H, K, V), torch.float32, q.device, contiguous=True)
+    _want("slots", slots, (B,), torch.int32, q.device, contiguous=True)
+    _want("o", o, v.shape, q.dtype, q.device)
+
+    def strides(name, t, last=True):
+        s = _gdr_stride(name, t.unsqueeze(2), last)
+        return GdrStride(s.b, s.h, 0)
+
+    if o is not None:
+        strides("o", o)
+    sq, sk, sv, sg, sb = strides("q", q), strides("k", k), strides("v", v), strides("g", g, False), \
+        strides("beta", beta, False)
+    _need_cuda(q)
+    with _on(q.device, stream, q, k, v, g, beta, S, slots, o) as cs:
+        o = torch.empty_like(v) if o is None else o
+        p = GdrStepParams(B, HK, H, K, V, S.shape[0], code, sq, sk, sv, sg, sb, strides("o", o))
+        st = lib().mlstm_gdr_step(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(slots),
+                                  _ptr(S), _ptr(o), cs)
+    if st != 0:
+        raise MlstmError(st, "mlstm_gdr_step")
+    return o
+
+
+def gdr_bwd(q, k, v, g, beta, do, S0=None, dS=None, *, seq_offsets=None, workspace=None, stream=None):
+    """Gradients of the gated delta rule (mlstm_gdr_bwd): gdr_fwd's inputs, do [B,H,T,V] and dS
+    [N,H,K,V] fp32 (the gradient of the final states) or None.  Returns a dict: dq, dk, dv in the inputs'
+    type, laid out like them where they fill their memory; dg, dbeta [B,H,T] and dS0 [N,H,K,V] fp32.
+    Gradients of tokens that no packed sequence holds are zero."""
+    B, HK, H, T, K, V, N = _gdr_shapes(q, k, v, g, beta, seq_offsets)
+    _want("do", do, v.shape, q.dtype, q.device)
+    _want("S0", S0, (N, H, K, V), torch.float32, q.device, contiguous=True)
+    _want("dS", dS, (N, H, K, V), torch.float32, q.device, contiguous=True)
+    p = gdr_params(q, k, v, g, beta, do, seq_offsets, "auto")
+    _need_cuda(q)
+    with _on(q.device, stream, q, k, v, g, beta, do, S0, dS, seq_offsets, workspace) as cs:
+        packed = seq_offsets is not None
+        f32 = dict(dtype=torch.float32, device=q.device)
+        out = {"dq": _like(q, packed), "dk": _like(k, packed), "dv": _like(v, packed),
+               "dg": (torch.zeros if packed else torch.empty)((B, H, T), **f32),
+               "dbeta": (torch.zeros if packed else torch.empty)((B, H, T), **f32),
+               "dS0": torch.empty((N, H, K, V), **f32)}
+        workspace, ws_len = _workspace(workspace, gdr_bwd_workspace_size(p), q.device)
+        st = lib().mlstm_gdr_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
+                                 _ptr(seq_offsets), _ptr(do), _ptr(dS), _gdr_stride("dq", out["dq"]),
+                                 _gdr_stride("dk", out["dk"]), _gdr_stride("dv", out["dv"]), _ptr(out["dq"]),
+                                 _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]),
+                                 _ptr(out["dS0"]), _ptr(workspace), ctypes.c_size_t(ws_len), cs)
+    if st != 0:
+        raise MlstmError(st, "mlstm_gdr_bwd")
+    return out
+
+
+def _rows(name, t):
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} is [..., D]")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.numel() // t.shape[-1], t.shape[-1]
+
+
+def rms_norm(x, residual=None, weight=None, eps: float = 1e-6, *, quant=None, group: int = 0, residual_out=None,
+             y=None, scales=None, stream=None):
+    """Root-mean-square norm of x + residual (mlstm_rms_norm): x, residual [..., D] fp32 or bf16, weight
+    [D] fp32 or None.  quant None (y in x's type), "e4m3" or "int8" with fp32 scales for each row (group 0)
+    or each 128 channels of it (group 128): y * scale stands for the output.  residual_out may be residual
+    (in place).  Returns (y, residual_out, scales [..., groups]); the latter two None where there is no
+    residual or no quant."""
+    rows, D = _rows("x", x)
+    code = _dtype_code(x)
+    if quant not in RMS_QUANT:
+        raise ValueError(f"quant must be one of {tuple(RMS_QUANT)}, got {quant!r}")
+    if quant is not None and group not in (0, 128):
+        raise ValueError(f"group must be 0 or 128, got {group}")
+    ytype = {None: x.dtype, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}[quant]
+    groups = (-(-D // group) if group else 1,)
+    _want("residual", residual, x.shape, x.dtype, x.device, contiguous=True)
+    _want("weight", weight, (D,), torch.float32, x.device, contiguous=True)
+    _want("residual_out", residual_out, x.shape, x.dtype, x.device, contiguous=True)
+    _want("y", y, x.shape, ytype, x.device, contiguous=True)
+    _want("scales", scales, x.shape[:-1] + groups, torch.float32, x.device, contiguous=True)
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if quant is None and scales is not None:
+        raise ValueError("scales without quant")
+    _need_cuda(x)
+    with _on(x.device, stream, x, residual, weight, residual_out, y, scales) as cs:
+        y = torch.empty(x.shape, dtype=ytype, device=x.device) if y is None else y
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(x)
+        if quant is not None and scales is None:
+            scales = torch.empty(x.shape[:-1] + groups, dtype=torch.float32, device=x.device)
+        p = RmsParams(rows, D, code, RMS_QUANT[quant], group if quant else 0, eps)
+        st = lib().mlstm_rms_norm(ctypes.byref(p), _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y),
+                                  _ptr(scales), cs)
+    if st != 0:
+        raise MlstmError(st, "mlstm_rms_norm")
+    return y, residual_out, scales
+
+
+def rms_norm_bwd(dy, r, weight=None, eps: float = 1e-6, dresidual=None, *, dx=None, return_dweight: bool = True,
+                 workspace=None, stream=None):
+    """Gradients of rms_norm without quant (mlstm_rms_norm_bwd): r [..., D] is the sum that was normalised
+    (residual_out, or x without a residual), dresidual the gradient of residual_out or None.  dx, the
+    gradient of x and of residual alike, may be dy or dresidual (in place).  Returns (dx, dweight [D] fp32
+    or None)."""
+    rows, D = _rows("r", r)
+    code = _dtype_code(r)
+    _want("dy", dy, r.shape, r.dtype, r.device, contiguous=True)
+    _want("weight", weight, (D,), torch.float32, r.device, contiguous=True)
+    _want("dresidual", dresidual, r.shape, r.dtype, r.device, contiguous=True)
+    _want("dx", dx, r.shape, r.dtype, r.device, contiguous=True)
+    _need_cuda(r)
+    with _on(r.device, stream, dy, r, weight, dresidual, dx, workspace) as cs:
+        dx = torch.empty_like(r) if dx is None else dx
+        dweight = torch.empty(D, dtype=torch.float32, device=r.device) if return_dweight else None
+        p = RmsParams(rows, D, code, 0, 0, eps)
+        need = int(lib().mlstm_rms_norm_bwd_workspace_size(ctypes.byref(p))) if return_dweight else 0
+        workspace, ws_len = _workspace(workspace, need, r.device)
+        st = lib().mlstm_rms_norm_bwd(ctypes.byref(p), _ptr(dy), _ptr(r), _ptr(weight), _ptr(dresidual), _ptr(dx),
+                                      _ptr(dweight), _ptr(workspace), ctypes.c_size_t(ws_len), cs)
+    if st != 0:
+        raise MlstmError(st, "mlstm_rms_norm_bwd")
+    return dx, dweight

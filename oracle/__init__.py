@@ -640,3 +640,64 @@ def state_bytes(layers: int, heads: int, dqk: int, dv: int, bytes_per_value: int
     normaliser and one stabiliser scalar (xLSTM 7B "Modelled costs": the state
     does not grow with context)."""
     return layers * heads * (dqk * dv + dqk + 1) * bytes_per_value
+
+
+def _gdr_spread(q, k, H):
+    """q, k [B,HK,T,K] as every value head reads them."""
+    group = H // q.shape[1]
+    return np.repeat(q, group, axis=1), np.repeat(k, group, axis=1)
+
+
+def gdr_sequential(q, k, v, g, beta, S0=None):
+    """The gated delta rule (the reduction b = w = beta 1 of ``gdn2_sequential`` with one decay per head
+    and token), fp64, one token at a time:
+
+        S' = e^{g_t} S;  r = S'^T k_t;  S = S' + beta_t k_t (v_t - r)^T;  o_t = S^T q_t
+
+    q, k [B,HK,T,K], v [B,H,T,V], g, beta [B,H,T], S0 [B,H,K,V] or None; value head h reads head
+    h / (H / HK) of q and k.  Returns (o [B,H,T,V], S_T [B,H,K,V])."""
+    q, k, v, g, beta = (np.asarray(x, dtype=np.float64) for x in (q, k, v, g, beta))
+    B, H, T, V = v.shape
+    q, k = _gdr_spread(q, k, H)
+    S = np.zeros((B, H, q.shape[-1], V)) if S0 is None else np.array(S0, dtype=np.float64)
+    o = np.zeros((B, H, T, V))
+    for t in range(T):
+        Sd = np.exp(g[:, :, t])[..., None, None] * S
+        r = np.einsum("bhkv,bhk->bhv", Sd, k[:, :, t])
+        S = Sd + np.einsum("bhk,bhv->bhkv", k[:, :, t], beta[:, :, t, None] * (v[:, :, t] - r))
+        o[:, :, t] = np.einsum("bhkv,bhk->bhv", S, q[:, :, t])
+    return o, S
+
+
+def gdr_sequential_backward(q, k, v, g, beta, do, S0=None, dS=None):
+    """Reverse-mode differentiation of the steps of ``gdr_sequential``, fp64: do [B,H,T,V], dS [B,H,K,V]
+    (gradient of S_T) or None.  Returns a dict dq, dk [B,HK,T,K], dv, dg, dbeta, dS0."""
+    q, k, v, g, beta, do = (np.asarray(x, dtype=np.float64) for x in (q, k, v, g, beta, do))
+    B, H, T, V = v.shape
+    HK, K = q.shape[1], q.shape[-1]
+    q, k = _gdr_spread(q, k, H)
+    S = np.zeros((B, H, K, V)) if S0 is None else np.array(S0, dtype=np.float64)
+    steps = []
+    for t in range(T):
+        Sd = np.exp(g[:, :, t])[..., None, None] * S
+        z = v[:, :, t] - np.einsum("bhkv,bhk->bhv", Sd, k[:, :, t])
+        S = Sd + np.einsum("bhk,bhv->bhkv", k[:, :, t], beta[:, :, t, None] * z)
+        steps.append((Sd, z, S))
+    D = np.zeros((B, H, K, V)) if dS is None else np.array(dS, dtype=np.float64)
+    dq, dk = np.zeros((B, H, T, K)), np.zeros((B, H, T, K))
+    dv, dg, dbeta = np.zeros((B, H, T, V)), np.zeros((B, H, T)), np.zeros((B, H, T))
+    for t in reversed(range(T)):
+        Sd, z, S = steps[t]
+        u = beta[:, :, t, None] * z
+        D = D + np.einsum("bhk,bhv->bhkv", q[:, :, t], do[:, :, t])
+        dq[:, :, t] = np.einsum("bhkv,bhv->bhk", S, do[:, :, t])
+        du = np.einsum("bhkv,bhk->bhv", D, k[:, :, t])
+        dbeta[:, :, t] = (du * z).sum(-1)
+        dz = beta[:, :, t, None] * du
+        dv[:, :, t] = dz
+        dk[:, :, t] = np.einsum("bhkv,bhv->bhk", D, u) - np.einsum("bhkv,bhv->bhk", Sd, dz)
+        D = D - np.einsum("bhk,bhv->bhkv", k[:, :, t], dz)
+        dg[:, :, t] = (D * Sd).sum((-1, -2))
+        D = np.exp(g[:, :, t])[..., None, None] * D
+    shared = lambda x: x.reshape(B, HK, H // HK, T, K).sum(2)
+    return {"dq": shared(dq), "dk": shared(dk), "dv": dv, "dg": dg, "dbeta": dbeta, "dS0": D}

@@ -1,0 +1,308 @@
+"""The gated delta rule (mlstm_gdr_fwd, mlstm_gdr_step) against its token-by-token oracle in 64 bits.
+
+Tolerances.  fp32 arithmetic with about eight roundings a token and value (two products over K in partial
+sums, the decay, the update); an error made at one token decays with the state, at most 128 tokens of it
+count for the decays drawn here: 8 * 128 * 2^-24 < 2^-14 of the largest value of a head's state or
+output.  Outputs in bf16 add half a step, 2^-8 of the value."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from linear_recurrent_token_b200 import inputs, mlstm
+from tests.helpers import TORCH_DTYPE, Guarded, dev, slice_relerr
+
+pytestmark = pytest.mark.gpu
+
+F32 = 2.0 ** -14
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+
+
+def to_dev(inp, dtype):
+    td = TORCH_DTYPE[dtype]
+    t = {n: dev(inp[n], td) for n in ("q", "k", "v")}
+    return t | {n: dev(inp[n]) for n in ("g", "beta", "S0")}
+
+
+def close(x, ref, dtype, rel=F32):
+    """Elementwise: half a step of the value, and rel of the head's largest."""
+    x, ref = x.double().cpu().numpy(), np.asarray(ref)
+    assert x.shape == ref.shape
+    big = np.abs(ref).max(axis=(-1, -2), keepdims=True) if ref.size else ref
+    bad = ~(np.abs(x - ref) <= HALF[dtype] * np.abs(ref) + rel * big + 1e-30)
+    assert not bad.any(), float((np.abs(x - ref) / (big + 1e-30)).max())
+
+
+SHAPES = [  # B, HK, H, T, K, V
+    (1, 1, 1, 1, 8, 8), (2, 1, 3, 2, 16, 24), (1, 2, 2, 17, 64, 40), (2, 2, 4, 31, 32, 32), (1, 1, 2, 63, 40, 88),
+    (1, 2, 2, 64, 64, 64), (2, 1, 1, 65, 128, 128), (1, 2, 4, 129, 96, 48), (1, 1, 1, 300, 128, 256),
+    (1, 1, 2, 200, 120, 16),
+]
+
+
+@pytest.mark.parametrize("mode", ["recurrent", "chunk", "auto"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("state", [True, False])
+def test_forward(shape, dtype, mode, state):
+    inp = inputs.gdr_inputs(*shape, dtype, seed=sum(shape), with_state=state)
+    B, HK, H, T, K, V = shape
+    t = to_dev(inp, dtype)
+    o, S = Guarded((B, H, T, V), TORCH_DTYPE[dtype]), Guarded((B, H, K, V), torch.float32)
+    mlstm.gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["S0"], mode=mode, o=o.t, S_out=S.t)
+    o_ref, S_ref = oracle.gdr_sequential(*(inp[n] for n in ("q", "k", "v", "g", "beta", "S0")))
+    close(o.t, o_ref, dtype)
+    close(S.t, S_ref, "f32")
+    assert o.intact() and S.intact()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_wide_keys(dtype):
+    inp = inputs.gdr_inputs(1, 1, 2, 70, 256, 72, dtype, seed=3)
+    t = to_dev(inp, dtype)
+    o, S = mlstm.gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["S0"])
+    o_ref, S_ref = oracle.gdr_sequential(*(inp[n] for n in ("q", "k", "v", "g", "beta", "S0")))
+    close(o, o_ref, dtype)
+    close(S, S_ref, "f32")
+
+
+def packed(inp, lengths):
+    """The oracle over each sequence of a packed batch; offsets."""
+    at, o, S = 0, np.zeros_like(inp["v"], dtype=np.float64), []
+    offsets = [0]
+    for n, x in enumerate(lengths):
+        sl = {m: inp[m][:, :, at:at + x] for m in ("q", "k", "v", "g", "beta")}
+        o[:, :, at:at + x], s = oracle.gdr_sequential(*(sl[m] for m in ("q", "k", "v", "g", "beta")),
+                                                      inp["S0"][n:n + 1])
+        S.append(s[0])
+        at += x
+        offsets.append(at)
+    return o, np.stack(S), torch.tensor(offsets, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("mode", ["recurrent", "chunk"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths,T", [((5, 0, 70, 1, 64, 0), 147), ((0, 0), 3), ((63, 65), 128), ((130,), 130)])
+def test_packed_sequences(lengths, T, dtype, mode):
+    inp = inputs.gdr_inputs(1, 2, 4, T, 64, 48, dtype, seed=T)
+    rng = np.random.default_rng(T)
+    inp["S0"] = (0.1 * rng.standard_normal((len(lengths), 4, 64, 48))).astype(np.float32)
+    o_ref, S_ref, off = packed(inp, lengths)
+    t = to_dev(inp, dtype)
+    o = Guarded((1, 4, T, 48), TORCH_DTYPE[dtype])
+    o.t.fill_(7.0)
+    _, S = mlstm.gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["S0"], seq_offsets=off, mode=mode, o=o.t)
+    used = sum(lengths)
+    close(o.t[:, :, :used], o_ref[:, :, :used], dtype)
+    assert bool((o.t[:, :, used:] == 7.0).all()) and o.intact()
+    close(S, S_ref, "f32")
+    fresh, _ = mlstm.gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["S0"], seq_offsets=off, mode=mode)
+    assert bool((fresh[:, :, used:] == 0).all()) and torch.equal(fresh[:, :, :used], o.t[:, :, :used])
+
+
+@pytest.mark.parametrize("mode", ["recurrent", "chunk"])
+def test_offsets_out_of_order_stay_inside(mode):
+    """Offsets that leave the tokens or fall are bounded: finite results, guards intact."""
+    inp = inputs.gdr_inputs(1, 1, 2, 90, 32, 16, "bf16", seed=2)
+    t = to_dev(inp, "bf16")
+    for bad in ([-5, 40, 1000], [80, 10, 90], [2**31 - 1, -2**31, 5], [91, 92, 93]):
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        o, S = Guarded((1, 2, 90, 16), torch.bfloat16), Guarded((2, 2, 32, 16), torch.float32)
+        o.t.zero_()
+        S0 = torch.zeros(2, 2, 32, 16, device="cuda")
+        mlstm.gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], S0, seq_offsets=off, mode=mode, o=o.t, S_out=S.t)
+        assert o.intact() and S.intact() and bool(torch.isfinite(S.t).all())
+
+
+@pytest.mark.parametrize("mode", ["recurrent", "chunk"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_strided_views(dtype, mode):
+    """Slices of one projection [B,T,width], gates [B,T,H], and one key row for all tokens (stride 0)."""
+    B, HK, H, T, K, V = 2, 2, 4, 77, 32, 24
+    inp = inputs.gdr_inputs(B, HK, H, T, K, V, dtype, seed=8)
+    inp["k"][:] = inp["k"][:, :, :1]
+    t = to_dev(inp, dtype)
+    fused = torch.cat([t["q"].transpose(1, 2).reshape(B, T, -1), t["v"].transpose(1, 2).reshape(B, T, -1)], -1)
+    q = fused[..., :HK * K].view(B, T, HK, K).transpose(1, 2)
+    v = fused[..., HK * K:].view(B, T, H, V).transpose(1, 2)
+    k = t["k"][:, :, :1].expand(B, HK, T, K)
+    g, beta = (t[n].transpose(1, 2).contiguous().transpose(1, 2) for n in ("g", "beta"))
+    o = torch.empty(B, T, H, V, dtype=q.dtype, device="cuda").transpose(1, 2)
+    assert not q.is_contiguous() and k.stride(2) == 0
+    _, S = mlstm.gdr_fwd(q, k, v, g, beta, t["S0"], mode=mode, o=o)
+    o2, S2 = mlstm.gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["S0"], mode=mode)
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    o_ref, S_ref = oracle.gdr_sequential(*(inp[n] for n in ("q", "k", "v", "g", "beta", "S0")))
+    close(o, o_ref, dtype)
+    close(S, S_ref, "f32")
+
+
+@pytest.mark.parametrize("mode", ["recurrent", "chunk"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gate_extremes(dtype, mode):
+    """Full resets, decays down to e^-90, no decay at all, write strengths 0, 1 and 2."""
+    inp = inputs.gdr_inputs(1, 2, 2, 150, 64, 32, dtype, seed=12)
+    rng = np.random.default_rng(1)
+    inp["g"][0, 0] = rng.choice([0.0, -np.inf, -90.0, -5.0, -1e-4, -1e30], 150)
+    inp["beta"][:] = rng.choice([0.0, 1.0, 2.0], (1, 2, 150))
+    t = to_dev(inp, dtype)
+    o, S = mlstm.gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["S0"], mode=mode)
+    o_ref, S_ref = oracle.gdr_sequential(*(inp[n] for n in ("q", "k", "v", "g", "beta", "S0")))
+    close(o, o_ref, dtype)
+    close(S, S_ref, "f32")
+
+
+@pytest.mark.parametrize("mode", ["recurrent", "chunk"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [1e-12, 1e12])
+def test_scales_of_the_inputs(dtype, mode, scale):
+    """Values and states far from one; k stays of unit length, q takes the other end."""
+    inp = inputs.gdr_inputs(1, 1, 2, 100, 64, 32, "f64", seed=13)
+    for n, f in (("v", scale), ("S0", scale), ("q", 1 / scale)):
+        inp[n] = inp[n] * f
+    for n in ("q", "k", "v"):
+        inp[n] = inputs.round_to(inp[n], dtype)
+    t = to_dev(inp, dtype)
+    inp = {n: x.double().cpu().numpy() for n, x in t.items()}
+    o, S = mlstm.gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["S0"], mode=mode)
+    o_ref, S_ref = oracle.gdr_sequential(*(inp[n] for n in ("q", "k", "v", "g", "beta", "S0")))
+    close(o, o_ref, dtype)
+    close(S, S_ref, "f32")
+
+
+@pytest.mark.parametrize("mode", ["recurrent", "chunk"])
+def test_values_that_are_not_finite_stay_in_their_head(mode):
+    inp = inputs.gdr_inputs(2, 2, 2, 80, 64, 32, "bf16", seed=14)
+    t = to_dev(inp, "bf16")
+    o1, S1 = mlstm.gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["S0"], mode=mode)
+    t["v"][0, 1, 40, 3] = float("nan")
+    t["g"][1, 0, 70] = float("nan")
+    o2, S2 = mlstm.gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["S0"], mode=mode)
+    for a, b in ((o1, o2), (S1, S2)):
+        assert torch.equal(a[0, 0], b[0, 0]) and torch.equal(a[1, 1], b[1, 1])
+    assert bool(torch.isnan(o2[0, 1, 40:, 3]).all()) and bool(torch.isnan(S2[1, 0]).all())
+    assert bool(torch.isfinite(o2[1, 0, :64].float()).all())
+
+
+def test_no_tokens_and_state_in_place():
+    q = torch.empty(2, 1, 0, 16, device="cuda")
+    v = torch.empty(2, 2, 0, 8, device="cuda")
+    g = torch.empty(2, 2, 0, device="cuda")
+    S0 = torch.randn(2, 2, 16, 8, device="cuda")
+    _, S = mlstm.gdr_fwd(q, q, v, g, g, S0)
+    assert torch.equal(S, S0)
+    _, S = mlstm.gdr_fwd(q, q, v, g, g)
+    assert bool((S == 0).all())
+    for mode in ("recurrent", "chunk"):
+        t = to_dev(inputs.gdr_inputs(2, 1, 2, 70, 16, 8, "bf16", seed=3), "bf16")
+        o, S = mlstm.gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["S0"], mode=mode)
+        o2, S2 = mlstm.gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["S0"], mode=mode, S_out=t["S0"])
+        assert S2 is t["S0"] and torch.equal(S, S2) and torch.equal(o, o2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,HK,H,K,V", [(1, 1, 1, 8, 8), (3, 2, 4, 64, 40), (2, 1, 3, 128, 128), (5, 2, 2, 256, 256),
+                                        (2, 1, 1, 100 - 4, 24), (90, 2, 4, 128, 128), (300, 2, 2, 32, 64)])
+def test_step(B, HK, H, K, V, dtype):
+    inp = inputs.gdr_inputs(B, HK, H, 1, K, V, dtype, seed=K + V)
+    t = to_dev(inp, dtype)
+    one = {n: t[n][:, :, 0] for n in ("q", "k", "v", "g", "beta")}
+    S = Guarded((B, H, K, V), torch.float32)
+    S.fill(t["S0"])
+    o = Guarded((B, H, V), TORCH_DTYPE[dtype])
+    mlstm.gdr_step(*one.values(), S.t, o=o.t)
+    o_ref, S_ref = oracle.gdr_sequential(*(inp[n] for n in ("q", "k", "v", "g", "beta", "S0")))
+    close(o.t[:, :, None], o_ref, dtype)
+    close(S.t, S_ref, "f32")
+    assert o.intact() and S.intact()
+
+
+def test_step_with_slots_padding_and_a_slot_named_twice():
+    B, HK, H, K, V, pool = 9, 1, 2, 64, 72, 12
+    inp = inputs.gdr_inputs(B, HK, H, 1, K, V, "bf16", seed=31)
+    t = to_dev(inp, "bf16")
+    one = {n: t[n][:, :, 0] for n in ("q", "k", "v", "g", "beta")}
+    slots = [3, -1, 11, 3, 0, 12, 3, 11, -2**31]
+    S0 = torch.randn(pool, H, K, V, device="cuda") * 0.1
+    S = S0.clone()
+    o = mlstm.gdr_step(*one.values(), S, slots=torch.tensor(slots, dtype=torch.int32, device="cuda"))
+    ref = S0.double().cpu().numpy()
+    for b, s in enumerate(slots):
+        if not 0 <= s < pool:
+            assert bool((o[b] == 0).all())
+            continue
+        sl = slice(b, b + 1)
+        o_ref, new = oracle.gdr_sequential(*(inp[n][sl] for n in ("q", "k", "v", "g", "beta")), ref[s:s + 1])
+        ref[s] = new[0]
+        close(o[sl][:, :, None], o_ref, "bf16")
+    close(S, ref, "f32")
+    untouched = [s for s in range(pool) if s not in slots]
+    assert torch.equal(S[untouched], S0[untouched])
+
+
+def test_steps_continue_a_prefill():
+    """A prefill and single tokens after it give what one prefill over all of them gives."""
+    inp = inputs.gdr_inputs(3, 2, 4, 75, 64, 32, "bf16", seed=41)
+    t = to_dev(inp, "bf16")
+    o_ref, S_ref = oracle.gdr_sequential(*(inp[n] for n in ("q", "k", "v", "g", "beta", "S0")))
+    head = {n: t[n][:, :, :70] for n in ("q", "k", "v", "g", "beta")}
+    _, S = mlstm.gdr_fwd(*head.values(), t["S0"])
+    for i in range(70, 75):
+        o = mlstm.gdr_step(*(t[n][:, :, i] for n in ("q", "k", "v", "g", "beta")), S)
+        close(o[:, :, None], o_ref[:, :, i:i + 1], "bf16")
+    close(S, S_ref, "f32")
+
+
+def test_captured_replayed_and_on_another_stream():
+    t = to_dev(inputs.gdr_inputs(2, 2, 2, 200, 64, 64, "bf16", seed=51), "bf16")
+    a = [t[n] for n in ("q", "k", "v", "g", "beta", "S0")]
+    ref = {m: mlstm.gdr_fwd(*a, mode=m) for m in ("recurrent", "chunk")}
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):  # two graphs, each with its own workspace
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append({m: mlstm.gdr_fwd(*a, mode=m) for m in ref})
+        graphs.append(graph)
+    for _ in range(2):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs.append({m: mlstm.gdr_fwd(*a, mode=m, stream=side) for m in ref})
+    torch.cuda.current_stream().wait_stream(side)
+    for out in outs:
+        for m in ref:
+            assert torch.equal(out[m][0], ref[m][0]) and torch.equal(out[m][1], ref[m][1])
+
+
+def test_a_block_of_norm_projections_recurrence_and_norm():
+    """The operators as a layer uses them: the pre-norm of the residual stream, projections (library
+    products of the caller), the gated delta rule on strided slices of them, the output's norm per head.
+    Against the same chain in 64 bits; each bf16 tensor between them is rounded there as well, the
+    projections' rounding can differ by one step: 2^-7 of the largest value through the rest."""
+    B, T, D, HK, H, K, V = 2, 90, 256, 2, 4, 32, 64
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    n = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    x, res = n(B, T, D).bfloat16(), n(B, T, D).bfloat16()
+    w, W = 1 + 0.1 * n(D), (n(D, 2 * HK * K + H * V) / 16).bfloat16()
+    g, beta = -torch.exp(n(B, T, H) - 3), torch.sigmoid(n(B, T, H))
+    y, r, _ = mlstm.rms_norm(x, res, w)
+    p = y @ W
+    cut = lambda lo, heads, d: p[..., lo:lo + heads * d].view(B, T, heads, d).transpose(1, 2)
+    q, k, v = cut(0, HK, K), cut(HK * K, HK, K), cut(2 * HK * K, H, V)
+    k = torch.nn.functional.normalize(k.float(), dim=-1).bfloat16()
+    q = (q.float() / K ** 0.5).bfloat16()
+    o = torch.empty(B, T, H, V, device="cuda", dtype=torch.bfloat16)
+    mlstm.gdr_fwd(q, k, v, g.transpose(1, 2), beta.transpose(1, 2), o=o.transpose(1, 2))
+    out, _, _ = mlstm.rms_norm(o)
+    r64 = x.double() + res.double()
+    y64 = r64 / torch.sqrt((r64 * r64).mean(-1, keepdim=True) + 1e-6) * w.double()
+    close(y.flatten(0, 1)[None], y64.flatten(0, 1)[None].cpu(), "bf16", 2.0 ** -19)
+    o_ref, _ = oracle.gdr_sequential(*(a.double().cpu().numpy() for a in (q, k, v, g.transpose(1, 2),
+                                                                          beta.transpose(1, 2))))
+    close(o.transpose(1, 2), o_ref, "bf16")
+    o64 = o.double()
+    out64 = o64 / torch.sqrt((o64 * o64).mean(-1, keepdim=True) + 1e-6)
+    close(out.flatten(0, 2)[None], out64.flatten(0, 2)[None].cpu(), "bf16", 2.0 ** -19)
