@@ -288,10 +288,6 @@ cudaError_t launch_step_t(const GdrStepArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-bool gdr_chunk_supported(int) { return false; }
-size_t gdr_chunk_workspace_bytes(const GdrArgs&) { return 0; }
-cudaError_t launch_gdr_chunk(const GdrArgs&, void*, cudaStream_t) { return cudaErrorNotSupported; }
-
 cudaError_t launch_gdr_recurrent(const GdrArgs& a, cudaStream_t stream) {
   return a.dtype ? launch_rec<__nv_bfloat16>(a, stream) : launch_rec<float>(a, stream);
 }
