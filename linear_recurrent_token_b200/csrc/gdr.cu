@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kRecThreads) gdr_recurrent_kernel(const GdrArg
   const int tid = threadIdx.x, part = tid & 3, col = tid >> 2, c = c0 + col;
   const int hk = h / (a.H / a.HK);
   long long lo = 0, len = a.T, b = n;
-  if (a.offsets) {  // offsets come from the device: bounded here to the tokens that there are
+  if (a.packed) {  // offsets come from the device: bounded here to the tokens that there are
     lo = min(max((long long)a.offsets[n], 0LL), (long long)a.T);
     len = min(max((long long)a.offsets[n + 1], lo), (long long)a.T) - lo;
     b = 0;

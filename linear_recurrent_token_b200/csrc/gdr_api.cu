@@ -85,6 +85,7 @@ GdrArgs gdr_args(const mlstm_gdr_params_t* p, const GdrShape& s) {
   GdrArgs a = {};
   a.N = (int)s.N, a.HK = p->HK, a.H = p->H, a.T = p->T, a.K = p->K, a.V = p->V;
   a.dtype = p->dtype == MLSTM_BF16 ? 1 : 0;
+  a.packed = p->num_seqs > 0 ? 1 : 0;
   a.sq = to_stride(p->q), a.sk = to_stride(p->k), a.sv = to_stride(p->v);
   a.sg = to_stride(p->g), a.sb = to_stride(p->beta), a.so = to_stride(p->o);
   return a;
@@ -149,7 +150,7 @@ mlstm_status_t mlstm_gdr_fwd(const mlstm_gdr_params_t* p, const void* q, const v
   }
   GdrArgs a = gdr_args(p, s);
   a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.S0 = S0, a.o = o, a.S_out = S_out;
-  a.offsets = p->num_seqs > 0 ? seq_offsets : nullptr;
+  a.offsets = seq_offsets;
   return done(s.chunk ? launch_gdr_chunk(a, workspace, (cudaStream_t)stream)
                       : launch_gdr_recurrent(a, (cudaStream_t)stream));
 }
@@ -191,12 +192,58 @@ mlstm_status_t mlstm_gdr_step(const mlstm_gdr_step_params_t* p, const void* q, c
   return done(launch_gdr_step(a, (cudaStream_t)stream));
 }
 
-size_t mlstm_gdr_bwd_workspace_size(const mlstm_gdr_params_t*) { return 0; }
-mlstm_status_t mlstm_gdr_bwd(const mlstm_gdr_params_t*, const void*, const void*, const void*, const float*,
-                             const float*, const float*, const int*, const void*, const float*, mlstm_gdr_stride_t,
-                             mlstm_gdr_stride_t, mlstm_gdr_stride_t, void*, void*, void*, float*, float*, float*,
-                             void*, size_t, mlstm_stream_t) {
-  return MLSTM_ERR_SHAPE;
+size_t mlstm_gdr_bwd_workspace_size(const mlstm_gdr_params_t* p) {
+  GdrShape s;
+  if (check_gdr(p, true, &s) != MLSTM_OK || !s.any) return 0;
+  return gdr_bwd_workspace_bytes(gdr_args(p, s));
+}
+
+mlstm_status_t mlstm_gdr_bwd(const mlstm_gdr_params_t* p, const void* q, const void* k, const void* v, const float* g,
+                             const float* beta, const float* S0, const int* seq_offsets, const void* dout,
+                             const float* dS, mlstm_gdr_stride_t s_dq, mlstm_gdr_stride_t s_dk,
+                             mlstm_gdr_stride_t s_dv, void* dq, void* dk, void* dv, float* dg, float* dbeta,
+                             float* dS0, void* workspace, size_t workspace_bytes, mlstm_stream_t stream) {
+  GdrShape s;
+  mlstm_status_t st = check_gdr(p, true, &s);
+  if (st != MLSTM_OK) return st;
+  if (!strides_ok(s_dq, p->B, p->HK, p->T, s.unit) || !strides_ok(s_dk, p->B, p->HK, p->T, s.unit) ||
+      !strides_ok(s_dv, p->B, p->H, p->T, s.unit) || !apart(s_dq, p->B, p->HK, p->T, p->K) ||
+      !apart(s_dk, p->B, p->HK, p->T, p->K) || !apart(s_dv, p->B, p->H, p->T, p->V))
+    return MLSTM_ERR_SHAPE;
+  if (s.any && (!q || !k || !v || !g || !beta || !dout || !dq || !dk || !dv || !dg || !dbeta)) return MLSTM_ERR_NULL;
+  if (p->num_seqs > 0 && !seq_offsets) return MLSTM_ERR_NULL;
+  const void* all[] = {q, k, v, S0, dout, dS, dq, dk, dv, dS0, workspace};
+  for (const void* x : all)
+    if (x && misaligned(x)) return MLSTM_ERR_ALIGN;
+  const void* words[] = {g, beta, seq_offsets, dg, dbeta};
+  for (const void* x : words)
+    if ((uintptr_t)x & 3) return MLSTM_ERR_ALIGN;
+  const size_t need = mlstm_gdr_bwd_workspace_size(p), bS = (size_t)s.N * p->H * p->K * p->V * 4;
+  const size_t gates = (size_t)p->B * p->H * p->T * 4;
+  const Range ins[] = {{q, span(p->q, p->B, p->HK, p->T, p->K) * s.es}, {k, span(p->k, p->B, p->HK, p->T, p->K) * s.es},
+                       {v, span(p->v, p->B, p->H, p->T, p->V) * s.es},  {g, span(p->g, p->B, p->H, p->T, 1) * 4},
+                       {beta, span(p->beta, p->B, p->H, p->T, 1) * 4},  {S0, bS},
+                       {seq_offsets, p->num_seqs > 0 ? (size_t)(p->num_seqs + 1) * 4 : 0},
+                       {dout, span(p->o, p->B, p->H, p->T, p->V) * s.es}, {dS, bS}};
+  const Out outs[] = {{{dq, span(s_dq, p->B, p->HK, p->T, p->K) * s.es}, nullptr},
+                      {{dk, span(s_dk, p->B, p->HK, p->T, p->K) * s.es}, nullptr},
+                      {{dv, span(s_dv, p->B, p->H, p->T, p->V) * s.es}, nullptr},
+                      {{dg, gates}, nullptr}, {{dbeta, gates}, nullptr}, {{dS0, bS}, nullptr},
+                      {{workspace, need}, nullptr}};
+  if (clash(ins, 9, outs, 7)) return MLSTM_ERR_ALIAS;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MLSTM_ERR_WORKSPACE;
+  if (s.N == 0 || p->H == 0) return MLSTM_OK;
+  if (!s.any) {  // no tokens: the initial states are the final ones
+    if (!dS0) return MLSTM_OK;
+    return done(dS ? cudaMemcpyAsync(dS0, dS, bS, cudaMemcpyDeviceToDevice, (cudaStream_t)stream)
+                   : cudaMemsetAsync(dS0, 0, bS, (cudaStream_t)stream));
+  }
+  GdrArgs a = gdr_args(p, s);
+  a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.S0 = S0, a.dout = dout, a.dS = dS;
+  a.offsets = seq_offsets;
+  a.sdq = to_stride(s_dq), a.sdk = to_stride(s_dk), a.sdv = to_stride(s_dv);
+  a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dS0 = dS0;
+  return done(launch_gdr_bwd(a, workspace, (cudaStream_t)stream));
 }
 
 static mlstm_status_t check_rms(const mlstm_rms_params_t* p, bool backward, int* group) {

@@ -8,30 +8,6 @@ namespace mlstm {
 namespace gdr {
 namespace {
 
-// 8 consecutive elements as fp32, zeros where !in
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool in, float (&x)[8]) {
-  if (!in) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack_bf16(u[e]);
-      x[2 * e] = f.x, x[2 * e + 1] = f.y;
-    }
-  } else {
-    const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-  }
-}
-
-// e^g as a sum's term: a decay below e^-10000 (and -infinity) is as good as a full reset, and sums of
-// 64 such terms keep every smaller one exactly in 64 bits.  NaN stays NaN.
-__device__ __forceinline__ double log_decay(float g) { return g < -1e4f ? -1e4 : (double)g; }
-
 constexpr int kPrepThreads = 256;
 constexpr int kMs = kL + 1;  // row pitch of the fp32 matrices
 
@@ -174,18 +150,11 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const GdrArgs a,
       const float* g = a.g + sq_.b * a.sg.b + h * a.sg.h;
       const float* be = a.beta + sq_.b * a.sb.b + h * a.sb.h;
       const int t = 2 * lane;
-      const double x0 = t < len ? log_decay(g[(t0 + t) * a.sg.t]) : 0.0;
-      const double x1 = t + 1 < len ? log_decay(g[(t0 + t + 1) * a.sg.t]) : 0.0;
-      double sum = x0 + x1;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const double y = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += y;
-      }
-      const double last = __shfl_sync(0xffffffffu, sum, 31), g0 = sum - x1;
-      G[t] = g0, G[t + 1] = sum;
-      fac[kGam * kL + t] = expf((float)g0), fac[kGam * kL + t + 1] = expf((float)sum);
-      fac[kW * kL + t] = expf((float)(last - g0)), fac[kW * kL + t + 1] = expf((float)(last - sum));
+      const double2 sum = cumulative(g, a.sg.t, t0, len, lane);
+      const double last = __shfl_sync(0xffffffffu, sum.y, 31);
+      G[t] = sum.x, G[t + 1] = sum.y;
+      fac[kGam * kL + t] = expf((float)sum.x), fac[kGam * kL + t + 1] = expf((float)sum.y);
+      fac[kW * kL + t] = expf((float)(last - sum.x)), fac[kW * kL + t + 1] = expf((float)(last - sum.y));
       fac[kBeta * kL + t] = t < len ? be[(t0 + t) * a.sb.t] : 0.f;
       fac[kBeta * kL + t + 1] = t + 1 < len ? be[(t0 + t + 1) * a.sb.t] : 0.f;
     }

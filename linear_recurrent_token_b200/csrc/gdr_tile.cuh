@@ -60,7 +60,7 @@ struct Seq {
 // takes records from lo / 64 + n on: they are disjoint and end below T / 64 + N.
 __device__ __forceinline__ Seq sequence(const GdrArgs& a, int n) {
   Seq s;
-  if (a.offsets) {
+  if (a.packed) {
     s.b = 0;
     s.lo = min(max((long long)a.offsets[n], 0LL), (long long)a.T);
     s.len = min(max((long long)a.offsets[n + 1], s.lo), (long long)a.T) - s.lo;
@@ -74,11 +74,11 @@ __device__ __forceinline__ Seq sequence(const GdrArgs& a, int n) {
   return s;
 }
 inline long long record_count(const GdrArgs& a) {
-  return a.offsets ? (long long)a.T / kL + a.N : (long long)a.N * ((a.T + kL - 1) / kL);
+  return a.packed ? (long long)a.T / kL + a.N : (long long)a.N * ((a.T + kL - 1) / kL);
 }
 // The sequence and chunk of a record; false where the record belongs to none.
 __device__ __forceinline__ bool find_chunk(const GdrArgs& a, long long rec, int* n, Seq* s, int* c) {
-  if (!a.offsets) {
+  if (!a.packed) {
     const long long per = (a.T + kL - 1) / kL;
     *n = (int)(rec / per);
   } else {
@@ -97,6 +97,24 @@ __device__ __forceinline__ bool find_chunk(const GdrArgs& a, long long rec, int*
   const long long chunk = rec - s->slot;
   *c = (int)chunk;
   return chunk >= 0 && chunk * kL < s->len;
+}
+
+// e^g as a sum's term: a decay below e^-10000 (and -infinity) is as good as a full reset, and sums of
+// 64 such terms keep every smaller one exactly in 64 bits.  NaN stays NaN.
+__device__ __forceinline__ double log_decay(float g) { return g < -1e4f ? -1e4 : (double)g; }
+
+// Cumulative log decays of the chunk that begins at token t0: lane has those of tokens 2 lane (x) and
+// 2 lane + 1 (y); no decay from `len` on.
+__device__ __forceinline__ double2 cumulative(const float* g, long long st, long long t0, int len, int lane) {
+  const int t = 2 * lane;
+  const double x0 = t < len ? log_decay(g[(t0 + t) * st]) : 0.0, x1 = t + 1 < len ? log_decay(g[(t0 + t + 1) * st]) : 0.0;
+  double sum = x0 + x1;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const double y = __shfl_up_sync(0xffffffffu, sum, d);
+    if (lane >= d) sum += y;
+  }
+  return make_double2(sum - x1, sum);
 }
 
 // ------------------------------------------------------------------------------------ small pieces
@@ -167,6 +185,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// 8 consecutive elements as fp32, zeros where !in
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool in, float (&x)[8]) {
+  if (!in) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+  } else if constexpr (sizeof(T) == 2) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack_bf16(u[e]);
+      x[2 * e] = f.x, x[2 * e + 1] = f.y;
+    }
+  } else {
+    const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+  }
+}
+
 // x, y (already scaled) as two fp16 parts
 __device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = pack(x, y);

@@ -11,16 +11,28 @@ namespace gdr {
 // a sequence, the final one) and by tile of 16 value columns.  Operands are stored in the order of the
 // fragments, 512 bytes a warp and step.
 struct Kept {
-  uint4* S;       // S^T at the chunk's start: [state][tile][part][KP / 16][32]
-  float* S_inv;   // [state][tile]
-  float4* Z;      // Z' [record][tile][8][32]
-  uint4* U;       // U^T: [record][tile][part][4][32]
+  uint4* S;       // S^T at the chunk's start: [state][tile][2 parts][KP / 16][32]
+  float* S_inv;   // the parts' scale: [state][tile]
+  float4* Z;      // Z': [record][tile][8][32]
+  uint4* U;       // U^T: [record][tile][NK parts][4][32]
   float* U_inv;   // [record][tile]
-  float* dots;    // dO . O over the tile's columns: [record][tile][64]
+  float* dots;    // dO . O, then dO . O - dV . V, over the tile's columns: [record][tile][64]
+  // of the pass backward
+  uint4* D;       // dS^T at the chunk's end: [record][tile][NK parts][KP / 16][32]
+  float* D_inv;   // [record][tile]
+  uint4* dV;      // dV^T: [record][tile][NK parts][4][32]
+  float* dV_inv;  // [record][tile]
+  float* dbeta;   // dY . Z' over the tile's columns: [record][tile][64]
+  float* ends;    // <dS, S> at the chunk's end over the tile's columns: [record][tile]
 };
-// S and U keep NK parts
+// Parts of an operand that only products rounded to the output's type read: one for bf16 (11 bits).
 template <typename T>
 constexpr int kept_parts() { return sizeof(T) == 4 ? 2 : 1; }
+
+// Four fragment registers of each of `steps` steps as they lie in a warp.
+__device__ __forceinline__ void keep(uint4* at, int step, int lane, const uint32_t (&r)[4]) {
+  at[step * 32 + lane] = make_uint4(r[0], r[1], r[2], r[3]);
+}
 
 template <typename T, int KP, bool P2>
 cudaError_t launch_prep(const GdrArgs& a, char* keys, char* records, cudaStream_t stream);
@@ -147,17 +159,15 @@ __global__ void __launch_bounds__(32 * W) gdr_walk_kernel(const GdrArgs a, const
   auto keep_state = [&](long long at, const Scale& sc) {  // at: the state's number
     if constexpr (GRAD) {
       if (tile >= tiles) return;
-      constexpr int NK = kept_parts<T>();
-      const size_t base = (((size_t)at * a.H + h) * tiles + tile);
+      const size_t base = ((size_t)at * a.H + h) * tiles + tile;
       if (lane == 0) kept.S_inv[base] = sc.inv;
 #pragma unroll
       for (int kk = 0; kk < KP / 16; ++kk) {
         uint32_t hi[4], lo[4];
         split_a(S[2 * kk], S[2 * kk + 1], sc.mul, hi, lo);
-        kept.S[((base * 2 + 0) * (KP / 16) + kk) * 32 + lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        kept.S[((base * 2 + 1) * (KP / 16) + kk) * 32 + lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        keep(kept.S + base * 2 * (KP / 16) * 32, kk, lane, hi);
+        keep(kept.S + (base * 2 + 1) * (KP / 16) * 32, kk, lane, lo);
       }
-      (void)NK;
     }
   };
 
@@ -240,8 +250,8 @@ __global__ void __launch_bounds__(32 * W) gdr_walk_kernel(const GdrArgs a, const
         constexpr int NK = kept_parts<T>();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          kept.U[((base * NK) * 4 + kk) * 32 + lane] = make_uint4(hi[kk][0], hi[kk][1], hi[kk][2], hi[kk][3]);
-          if (NK == 2) kept.U[((base * NK + 1) * 4 + kk) * 32 + lane] = make_uint4(lo[kk][0], lo[kk][1], lo[kk][2], lo[kk][3]);
+          keep(kept.U + base * NK * 128, kk, lane, hi[kk]);
+          if (NK == 2) keep(kept.U + (base * NK + 1) * 128, kk, lane, lo[kk]);
         }
       }
     }

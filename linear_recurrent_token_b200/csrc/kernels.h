@@ -150,8 +150,8 @@ struct GdrStride {
   long long b, h, t;
 };
 struct GdrArgs {
-  int N, HK, H, T, K, V, dtype;
-  const int* offsets;  // [N + 1] or NULL
+  int N, HK, H, T, K, V, dtype, packed;
+  const int* offsets;  // [N + 1] where packed
   const void *q, *k, *v;
   const float *g, *beta, *S0;
   void* o;
@@ -170,6 +170,8 @@ constexpr int kGdrChunkFrom = 32;
 bool gdr_chunk_supported(int K);
 size_t gdr_chunk_workspace_bytes(const GdrArgs& a);
 cudaError_t launch_gdr_chunk(const GdrArgs& a, void* ws, cudaStream_t stream);
+size_t gdr_bwd_workspace_bytes(const GdrArgs& a);
+cudaError_t launch_gdr_bwd(const GdrArgs& a, void* ws, cudaStream_t stream);
 
 // One token for each of B rows; row b's state is S[slots[b]] of `pool` states (slots NULL: S[b]).
 struct GdrStepArgs {
