@@ -9,51 +9,70 @@ namespace gdr {
 namespace {
 
 constexpr int kPrepThreads = 256;
-constexpr int kMs = kL + 1;  // row pitch of the fp32 matrices
+constexpr int kMs = kL + 4;  // row pitch of the fp32 matrices: a fragment's lanes meet no bank conflicts
 
 template <int KP, int NP>
 constexpr int prep_smem() {
-  return keys_bytes(KP, NP) + 2 * kL * kMs * 4 + 32 * 33 * 4 + kL * 8 + kFactorBytes + 2 * kL * 4;
+  constexpr int matrices = (2 * kL + 32) * kMs * 4;  // in the place of k and q
+  return (keys_bytes(KP, NP) > matrices ? keys_bytes(KP, NP) : matrices) + kL * 8 + kFactorBytes + 2 * kL * 4;
 }
 
-// dst (n x n, at r, c of R) = -(X + R22 b2 X), X = M21 + M21 b1 R11: joins two solved n x n diagonal blocks.
-template <int N>
-__device__ __forceinline__ void join_blocks(const float* M, float* R, const float* beta, float* X, int top, int t0,
-                                            int nthreads) {
-  const int low = top + N;
-  for (int e = t0; e < N * N; e += nthreads) {
-    const int t = e / N, s = e % N;
-    float x = M[(low + t) * kMs + top + s];
-    for (int i = s + 1; i < N; ++i) x = fmaf(M[(low + t) * kMs + top + i] * beta[top + i], R[(top + i) * kMs + top + s], x);
-    X[t * 33 + s] = x;
+// c += (A diag(b)) B for a 16 x 8 tile of c, k = 8 STEPS: fp32 matrices in shared memory (pitch kMs) as two
+// tf32 parts each, whose exponent is fp32's: no scaling.
+template <int STEPS>
+__device__ __forceinline__ void product_tf32(float (&c)[4], const float* A, const float* b, const float* B, int lane) {
+  const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    const int i = k * 8 + q;
+    const float b0 = b[i], b1 = b[i + 4];
+    uint32_t ah[4], al[4], bh[2], bl[2];
+    split_tf32(A[g * kMs + i] * b0, ah[0], al[0]);
+    split_tf32(A[(g + 8) * kMs + i] * b0, ah[1], al[1]);
+    split_tf32(A[g * kMs + i + 4] * b1, ah[2], al[2]);
+    split_tf32(A[(g + 8) * kMs + i + 4] * b1, ah[3], al[3]);
+    split_tf32(B[i * kMs + g], bh[0], bl[0]);
+    split_tf32(B[(i + 4) * kMs + g], bh[1], bl[1]);
+    mma_tf32(c, al, bh);
+    mma_tf32(c, ah, bl);
+    mma_tf32(c, ah, bh);
   }
 }
+
+// Joins the solved N x N diagonal blocks at `top` and top + N: with 1 the upper and 2 the lower block,
+//     X = M21 + M21 b1 R11,   R21 = -(X + R22 b2 X).
+// One warp a 16 x 8 tile (mt, nt); X has N rows of its own.  A barrier lies between the two halves.
 template <int N>
-__device__ __forceinline__ void join_rows(float* R, const float* beta, const float* X, int top, int t0, int nthreads) {
-  const int low = top + N;
-  for (int e = t0; e < N * N; e += nthreads) {
-    const int t = e / N, s = e % N;
-    float x = X[t * 33 + s];
-    for (int i = 0; i < t; ++i) x = fmaf(R[(low + t) * kMs + low + i] * beta[low + i], X[i * 33 + s], x);
-    R[(low + t) * kMs + top + s] = -x;
-  }
+__device__ __forceinline__ void join_half(bool second, const float* M, float* R, float* X, const float* beta, int top,
+                                          int mt, int nt, int lane) {
+  const int low = top + N, r = mt * 16 + (lane >> 2), cc = nt * 8 + 2 * (lane & 3);
+  const float* from = second ? X : M + low * kMs + top;
+  float c[4] = {from[r * kMs + cc], from[r * kMs + cc + 1], from[(r + 8) * kMs + cc], from[(r + 8) * kMs + cc + 1]};
+  if (second)
+    product_tf32<N / 8>(c, R + (low + mt * 16) * kMs + low, beta + low, X + nt * 8, lane);
+  else
+    product_tf32<N / 8>(c, M + (low + mt * 16) * kMs + top, beta + top, R + top * kMs + top + nt * 8, lane);
+  float* to = second ? R + low * kMs + top : X;
+  const float sign = second ? -1.f : 1.f;
+  to[r * kMs + cc] = sign * c[0], to[r * kMs + cc + 1] = sign * c[1];
+  to[(r + 8) * kMs + cc] = sign * c[2], to[(r + 8) * kMs + cc + 1] = sign * c[3];
 }
 
 // One block for each chunk and key head; the value heads that share it follow one another.  The two
-// 64 x 64 x KP products run on the tensor cores; the triangular solve is fp32: four 16 x 16 diagonal
-// blocks column by column, then two joins.
+// 64 x 64 x KP products run on the tensor cores; of the triangular solve, four 16 x 16 diagonal blocks go
+// row by row in fp32 and two rounds of joins on the tensor cores again.
 template <typename T, int KP, bool P2>
-__global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const GdrArgs a, char* keys, char* records) {
+__global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs a, char* keys, char* records) {
   constexpr int NP = sizeof(T) == 4 ? 2 : 1;
   extern __shared__ __align__(16) char smem[];
   char* sk = smem;  // k parts, then q parts
   char* sq = smem + keys_bytes(KP, NP) / 2;
-  float* M = reinterpret_cast<float*>(smem + keys_bytes(KP, NP));
+  float* M = reinterpret_cast<float*>(smem);  // once the products with k and q are in registers
   float* R = M + kL * kMs;
-  float* X = R + kL * kMs;
-  double* G = reinterpret_cast<double*>(X + 32 * 33);
-  float* fac = reinterpret_cast<float*>(G + kL);
+  float* X = R + kL * kMs;  // [32]
+  float* fac = reinterpret_cast<float*>(smem + prep_smem<KP, NP>()) - (kFactors + 2) * kL;
   float* pmax = fac + kFactors * kL;  // [2][64]
+  float2* G = reinterpret_cast<float2*>(fac) - kL;
   int n, c;
   Seq sq_;
   if (!find_chunk(a, blockIdx.x, &n, &sq_, &c)) return;
@@ -152,26 +171,27 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const GdrArgs a,
       const int t = 2 * lane;
       const double2 sum = cumulative(g, a.sg.t, t0, len, lane);
       const double last = __shfl_sync(0xffffffffu, sum.y, 31);
-      G[t] = sum.x, G[t + 1] = sum.y;
+      G[t] = two_parts(sum.x), G[t + 1] = two_parts(sum.y);
       fac[kGam * kL + t] = expf((float)sum.x), fac[kGam * kL + t + 1] = expf((float)sum.y);
       fac[kW * kL + t] = expf((float)(last - sum.x)), fac[kW * kL + t + 1] = expf((float)(last - sum.y));
       fac[kBeta * kL + t] = t < len ? be[(t0 + t) * a.sb.t] : 0.f;
       fac[kBeta * kL + t + 1] = t + 1 < len ? be[(t0 + t + 1) * a.sb.t] : 0.f;
     }
     __syncthreads();
+    // P, rows scaled, and M; blocks above the diagonal are never read
     float p[4][4], big[2] = {0.f, 0.f};
+    if (lower) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = r0 + (lane >> 2) + (e >> 1) * 8, s = c0 + j * 8 + (lane & 3) * 2 + (e & 1);
-        const float D = s <= t ? expf((float)(G[t] - G[s])) : 0.f;
-        p[j][e] = s <= t ? qk[j][e] * D : 0.f;
-        big[e >> 1] = fmaxf(big[e >> 1], fabsf(p[j][e]));
-        const float m = s < t ? kk_[j][e] * D : 0.f;
-        M[t * kMs + s] = m;
-        R[t * kMs + s] = 0.f;
-      }
+        for (int e = 0; e < 4; ++e) {
+          const int t = r0 + (lane >> 2) + (e >> 1) * 8, s = c0 + j * 8 + (lane & 3) * 2 + (e & 1);
+          const float D = s <= t ? decay_between(G[t], G[s]) : 0.f;
+          p[j][e] = s <= t ? qk[j][e] * D : 0.f;
+          big[e >> 1] = fmaxf(big[e >> 1], fabsf(p[j][e]));
+          M[t * kMs + s] = s < t ? kk_[j][e] * D : 0.f;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       big[i] = fmaxf(big[i], __shfl_xor_sync(0xffffffffu, big[i], 1));
@@ -179,7 +199,29 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const GdrArgs a,
       if ((lane & 3) == 0) pmax[(warp >> 2) * kL + r0 + (lane >> 2) + i * 8] = big[i];
     }
     __syncthreads();
-    // P, rows scaled; blocks above the diagonal are never read
+    const float* beta = fac + kBeta * kL;
+    if (lane < 16 && warp >= 4) {  // R: a 16 x 16 diagonal block a warp, a column a lane
+      const int top = (warp - 4) * 16, s = lane;
+      float y[16];  // beta_i R[i][s]
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        float m[16], x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < t; i += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(M + (top + t) * kMs + top + i);
+          m[i] = v.x, m[i + 1] = v.y, m[i + 2] = v.z, m[i + 3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < t; ++i) x[i & 3] = fmaf(m[i], y[i], x[i & 3]);
+        const float r = t > s ? -(M[(top + t) * kMs + top + s] + ((x[0] + x[1]) + (x[2] + x[3]))) : 0.f;
+        R[(top + t) * kMs + top + s] = r;
+        y[t] = beta[top + t] * r;
+      }
+    } else if (warp == 4 || warp == 6) {  // the blocks above the diagonal that the second join reads
+      const int top = (warp - 4) * 16;
+#pragma unroll
+      for (int t = 0; t < 16; ++t) R[(top + t) * kMs + top + lane] = 0.f;
+    }
     if (lower) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -196,53 +238,42 @@ __global__ void __launch_bounds__(kPrepThreads) gdr_prep_kernel(const GdrArgs a,
         }
       }
     }
-    // R: the 16 x 16 diagonal blocks, a thread a column
-    const float* beta = fac + kBeta * kL;
-    if (tid < kL) {
-      const int top = tid & ~15, s = tid & 15;
-      float y[16];  // beta_i R[i][s]
-#pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        float x = t > s ? M[(top + t) * kMs + top + s] : 0.f;
-#pragma unroll
-        for (int i = 0; i < t; ++i) x = fmaf(M[(top + t) * kMs + top + i], y[i], x);
-        x = t > s ? -x : 0.f;
-        R[(top + t) * kMs + top + s] = x;
-        y[t] = beta[top + t] * x;
-      }
-    }
     __syncthreads();
-    {
-      const int pair = tid >> 7, t1 = tid & 127;
-      join_blocks<16>(M, R, beta, X + pair * 16 * 33, pair * 32, t1, 128);
-      __syncthreads();
-      join_rows<16>(R, beta, X + pair * 16 * 33, pair * 32, t1, 128);
-      __syncthreads();
-      join_blocks<32>(M, R, beta, X, 0, tid, kPrepThreads);
-      __syncthreads();
-      join_rows<32>(R, beta, X, 0, tid, kPrepThreads);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (warp < 4) join_half<16>(half, M, R, X + (warp >> 1) * 16 * kMs, beta, (warp >> 1) * 32, 0, warp & 1, lane);
       __syncthreads();
     }
-    {  // R, rows scaled: four threads a row, 16 columns each
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      join_half<32>(half, M, R, X, beta, 0, warp >> 2, warp & 3, lane);
+      __syncthreads();
+    }
+    {  // R, rows scaled: four threads a row, 16 columns each, none above the diagonal's block
       const int row = tid >> 2, part = tid & 3;
+      const bool below = part * 16 <= row;
       float x[16], m = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[e] = R[row * kMs + part * 16 + e];
-        m = fmaxf(m, fabsf(x[e]));
+      for (int e = 0; e < 16; e += 4) {
+        const float4 v = below ? *reinterpret_cast<const float4*>(R + row * kMs + part * 16 + e)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
+        m = fmaxf(fmaxf(fmaxf(m, fabsf(v.x)), fmaxf(fabsf(v.y), fabsf(v.z))), fabsf(v.w));
       }
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const Scale sc = scale_of(m);
       if (part == 0) fac[kRInv * kL + row] = sc.inv;
+      if (below) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t hi[4], lo[4];
+        for (int i = 0; i < 2; ++i) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split(x[i * 8 + 2 * e] * sc.mul, x[i * 8 + 2 * e + 1] * sc.mul, hi[e], lo[e]);
-        const int at = piece_at<kL>(row, part * 16 + i * 8);
-        *reinterpret_cast<uint4*>(out + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(out + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          for (int e = 0; e < 4; ++e) split(x[i * 8 + 2 * e] * sc.mul, x[i * 8 + 2 * e + 1] * sc.mul, hi[e], lo[e]);
+          const int at = piece_at<kL>(row, part * 16 + i * 8);
+          *reinterpret_cast<uint4*>(out + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(out + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
       }
     }
     __syncthreads();

@@ -103,6 +103,14 @@ __device__ __forceinline__ bool find_chunk(const GdrArgs& a, long long rec, int*
 // 64 such terms keep every smaller one exactly in 64 bits.  NaN stays NaN.
 __device__ __forceinline__ double log_decay(float g) { return g < -1e4f ? -1e4 : (double)g; }
 
+// A sum in 64 bits as two fp32 parts, and the decay e^(a - b) between two of them: the difference keeps
+// fp32's relative accuracy however large the sums are.
+__device__ __forceinline__ float2 two_parts(double x) {
+  const float hi = (float)x;
+  return make_float2(hi, (float)(x - hi));
+}
+__device__ __forceinline__ float decay_between(float2 a, float2 b) { return expf((a.x - b.x) + (a.y - b.y)); }
+
 // Cumulative log decays of the chunk that begins at token t0: lane has those of tokens 2 lane (x) and
 // 2 lane + 1 (y); no decay from `len` on.
 __device__ __forceinline__ double2 cumulative(const float* g, long long st, long long t0, int len, int lane) {
@@ -149,6 +157,19 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// c += a b, tf32 operands
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// x in two tf32 parts (22 bits)
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  const float rest = x - __uint_as_float(hi);
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
 }
 
 // Lane addresses of ldmatrix.x4 on a tile whose rows are `row`-indexed from r0 and columns from c0:
