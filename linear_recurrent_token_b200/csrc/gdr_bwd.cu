@@ -13,193 +13,180 @@ namespace mlstm {
 namespace gdr {
 namespace {
 
-// A block takes 16 W value columns of one value head of one sequence, chunks from the last to the first.
-template <typename T, int KP, int W>
-__global__ void __launch_bounds__(32 * W) gdr_back_kernel(const GdrArgs a, const char* keys, const char* records,
-                                                          const Kept kept) {
-  using L = WalkStage<T, KP, W, true>;
-  constexpr int NP = L::NP, NK = kept_parts<T>();
+// A block takes 16 TN value columns of one value head of one sequence, chunks from the last to the first.
+template <typename T, int KP, int TN>
+__global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrArgs a, const char* keys,
+                                                                      const char* records, const Kept kept) {
+  using L = Stage<T, KP, TN, true>;
+  constexpr int NP = L::NP, NK = kept_parts<T>(), KS = KP / 64, threads = 32 * kQuarter * TN;
+  // In exchange: dS, then beta dU in its place; dO by P's scale; gam dV; gam dO.
+  constexpr int fy = L::fs;
   extern __shared__ __align__(128) char smem[];
   const int n = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tile = blockIdx.x * W + warp, tiles = (a.V + 15) / 16, col0 = blockIdx.x * 16 * W;
-  const int v0 = tile * 16, cols = min(16, a.V - v0);
+  const int local = warp / kQuarter, w = warp % kQuarter, tile = blockIdx.x * TN + local, tiles = (a.V + 15) / 16;
+  const int col0 = blockIdx.x * 16 * TN, v0 = tile * 16, cols = min(16, a.V - v0);
   const bool live = tile < tiles;
   const Seq s = sequence(a, n);
   const int chunks = (int)((s.len + kL - 1) / kL);
   const size_t state = ((size_t)n * a.H + h) * a.K * a.V;
   const int ra = lane >> 2, ca = 2 * (lane & 3);
+  char* mats = smem + L::chunks * L::chunk;
+  char* ex = mats + L::matrices + local * L::tile;
+  float* inv = reinterpret_cast<float*>(ex + L::inv);
 
-  float D[KP / 8][4];
+  float D[2 * KS][4];
 #pragma unroll
-  for (int j = 0; j < KP / 8; ++j)
+  for (int j = 0; j < 2 * KS; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int col = ra + (e >> 1) * 8, key = 8 * j + ca + (e & 1);
+      const int col = ra + (e >> 1) * 8, key = w * (KP / 4) + 8 * j + ca + (e & 1);
       D[j][e] = a.dS && col < cols && key < a.K ? a.dS[state + (size_t)key * a.V + v0 + col] : 0.f;
     }
-
-  const uint32_t smem_base = smem_u32(smem);
-  if (chunks > 0)
-    fetch_chunk<T, KP, W, true>(a, s, s.slot + chunks - 1, h, chunks - 1, col0, keys, records,
-                                smem_base + (L::stages == 2 ? ((chunks - 1) & 1) * L::bytes : 0));
+  auto slot = [&](int c) { return smem + (L::chunks == 2 ? (c & 1) * L::chunk : 0); };
+  if (chunks > 0) {
+    fetch_chunk<T, KP, TN, true>(a, s, s.slot + chunks - 1, h, chunks - 1, col0, keys, records, smem_u32(slot(chunks - 1)));
+    cp_commit();
+  }
   for (int c = chunks - 1; c >= 0; --c) {
     const long long rec = s.slot + c;
-    char* st = smem + (L::stages == 2 ? (c & 1) * L::bytes : 0);
-    const uint32_t su = smem_u32(st);
-    cp_wait_all();
-    __syncthreads();
-    if (L::stages == 2 && c > 0)
-      fetch_chunk<T, KP, W, true>(a, s, rec - 1, h, c - 1, col0, keys, records, smem_base + ((c - 1) & 1) * L::bytes);
-    const float* fac = reinterpret_cast<const float*>(st + L::factors);
     const size_t base = ((size_t)rec * a.H + h) * tiles + tile;
-
-    // x = (K dS)^T, and <dS, S> with the state that the forward pass left here
-    const Scale sd = scale_of(tile_max<KP / 8>(D));
-    float x[8][4], end = 0.f;
+    char* st = slot(c);
+    const float* fac = reinterpret_cast<const float*>(st + L::factors);
+    {
+      const Scale sc = scale_of(tile_max(D));
+      give<KS, 2>(D, sc, ex + L::fs, inv, w, lane);
+      if (live) {  // dS for the gradients of k, and <dS, S> with the state that the forward pass left here
+        const size_t after = ((size_t)(rec + n + 1) * a.H + h) * tiles + tile;
+        float end = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+        for (int i = 0; i < KS; ++i) {
+          uint4 hi, lo;
+          split_a(D[2 * i], D[2 * i + 1], sc.mul, hi, lo);
+          kept.D[(base * NK * (KP / 16) + w * KS + i) * 32 + lane] = hi;
+          if (NK == 2) kept.D[((base * NK + 1) * (KP / 16) + w * KS + i) * 32 + lane] = lo;
+          const uint4 sh = kept.S[(after * 2 * (KP / 16) + w * KS + i) * 32 + lane];
+          const uint4 sl = kept.S[((after * 2 + 1) * (KP / 16) + w * KS + i) * 32 + lane];
+          const uint32_t h4[4] = {sh.x, sh.y, sh.z, sh.w}, l4[4] = {sl.x, sl.y, sl.z, sl.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[j][e] = 0.f;
-    const size_t after = ((size_t)(rec + n + 1) * a.H + h) * tiles + tile;
-    if (live && lane == 0) kept.D_inv[base] = sd.inv;
+          for (int r = 0; r < 4; ++r) {
+            const float2 f = unpack(h4[r]), g = unpack(l4[r]);
+            end = fmaf(D[2 * i + (r >> 1)][(r & 1) * 2], f.x + g.x, end);
+            end = fmaf(D[2 * i + (r >> 1)][(r & 1) * 2 + 1], f.y + g.y, end);
+          }
+        }
 #pragma unroll
-    for (int kk = 0; kk < KP / 16; ++kk) {
-      uint32_t hi[4], lo[4];
-      split_a(D[2 * kk], D[2 * kk + 1], sd.mul, hi, lo);
-      if (live) {
-        keep(kept.D + base * NK * (KP / 16) * 32, kk, lane, hi);
-        if (NK == 2) keep(kept.D + (base * NK + 1) * (KP / 16) * 32, kk, lane, lo);
-        const uint4 sh = kept.S[(after * 2 * (KP / 16) + kk) * 32 + lane];
-        const uint4 sl = kept.S[((after * 2 + 1) * (KP / 16) + kk) * 32 + lane];
-        const uint32_t a4[4] = {sh.x, sh.y, sh.z, sh.w}, b4[4] = {sl.x, sl.y, sl.z, sl.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = unpack(a4[i]), g = unpack(b4[i]);
-          end = fmaf(D[2 * kk + (i >> 1)][(i & 1) * 2], f.x + g.x, end);
-          end = fmaf(D[2 * kk + (i >> 1)][(i & 1) * 2 + 1], f.y + g.y, end);
+        for (int d = 16; d > 0; d /= 2) end += __shfl_xor_sync(0xffffffffu, end, d);
+        if (lane == 0) {
+          kept.D_inv[base * kQuarter + w] = sc.inv;
+          kept.ends[base * kQuarter + w] = end * kept.S_inv[after * kQuarter + w];
         }
       }
-      rows_step<KP, NP, true>(x, hi, lo, su, kk, lane);
     }
+    cp_wait<0>();
+    __syncthreads();  // the chunk has come, dS is in exchange, and nobody is in the chunk behind
+    fetch_matrices<true, threads>(a, rec, h, records, smem_u32(mats));
+    cp_commit();
+    if (L::chunks == 2) {
+      if (c > 0) fetch_chunk<T, KP, TN, true>(a, s, rec - 1, h, c - 1, col0, keys, records, smem_u32(slot(c - 1)));
+      cp_commit();
+    }
+    // this quarter's share of dO by P's scale, and gam dO
+    float x[2][4], y[2][4];
+    {
+      float d[2][4];
+      read_columns<T, L::row>(d, st + L::dout + w * 16 * L::row + local * 16 * (int)sizeof(T), lane);
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) end += __shfl_xor_sync(0xffffffffu, end, d);
-    if (live && lane == 0) kept.ends[base] = end * kept.S_inv[after];
-
-    // dU = w (K dS) + P^T dO
-    uint32_t hi[4][4], lo[4][4];
-    float y[8][4];
-    const char* dt = st + L::dout + warp * 16 * (int)sizeof(T);
-    const uint32_t du = su + L::dout + warp * 16 * (int)sizeof(T);
-    read_columns<T, L::row>(y, dt, du, lane);
+      for (int j = 0; j < 2; ++j) {
+        const float2 pi = factor(fac + kPInv * kL, w * 16, j, lane), gq = factor(fac + kGQ * kL, w * 16, j, lane);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 w = factor(fac + kW * kL, j, lane), ki = factor(fac + kKInv * kL, j, lane);
-      const float2 pi = factor(fac + kPInv * kL, j, lane);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[j][e] *= sd.inv * (e & 1 ? w.y * ki.y : w.x * ki.x);
-        y[j][e] *= e & 1 ? pi.y : pi.x;
+        for (int e = 0; e < 4; ++e) {
+          x[j][e] = d[j][e] * (e & 1 ? pi.y : pi.x);
+          y[j][e] = d[j][e] * (e & 1 ? gq.y : gq.x);
+        }
       }
+      give<1, NP>(x, scale_of(tile_max(x)), ex + L::fu, inv + 2 * kQuarter, w, lane);
+      give<1, 2>(y, scale_of(tile_max(y)), ex + L::fz, inv + 4 * kQuarter, w, lane);
     }
-    const Scale sp = scale_of(tile_max<8>(y));
+    // dU = w (K dS) + P^T dO
+    by_keys<KP, NP, false, false>(x, y, ex + L::fs, inv, smem_u32(st), 0u, w, lane);
+    float4 z0 = make_float4(0.f, 0.f, 0.f, 0.f), z1 = z0;
+    if (live) z0 = kept.Z[(base * 8 + 2 * w) * 32 + lane], z1 = kept.Z[(base * 8 + 2 * w + 1) * 32 + lane];
+    cp_wait<L::chunks == 2 ? 1 : 0>();
+    __syncthreads();  // R and P have come, dO is in exchange, dS has been read
+    by_tokens<true, NP, 2>(y, ex + L::fu, inv + 2 * kQuarter, smem_u32(mats) + 2 * kTile, w, lane);
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) split_a(y[2 * kk], y[2 * kk + 1], sp.mul, hi[kk], lo[kk]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[j][e] = 0.f;
-    triangle<true, NP, 2>(y, hi, lo, su + L::record + 2 * kTile, lane);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 be = factor(fac + kBeta * kL, j, lane), ri = factor(fac + kRInv * kL, j, lane);
+    for (int j = 0; j < 2; ++j) {
+      const float2 wk = factor(fac + kWK * kL, w * 16, j, lane), be = factor(fac + kBeta * kL, w * 16, j, lane);
+      const float2 ri = factor(fac + kRInv * kL, w * 16, j, lane);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[j][e] = fmaf(y[j][e], sp.inv, x[j][e]);
+        x[j][e] = fmaf(x[j][e], e & 1 ? wk.y : wk.x, y[j][e]);
         y[j][e] = x[j][e] * (e & 1 ? be.y * ri.y : be.x * ri.x);
       }
     }
+    give<1, 2>(y, scale_of(tile_max(y)), ex + fy, inv + kQuarter, w, lane);
+    tile_barrier(local);  // beta dU is in exchange
     // dY = dU + R^T (beta dU), dV = beta dY
-    const Scale sr = scale_of(tile_max<8>(y));
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) split_a(y[2 * kk], y[2 * kk + 1], sr.mul, hi[kk], lo[kk]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[j][e] = 0.f;
-    triangle<true, 2, 2>(y, hi, lo, su + L::record, lane);
-    const int len = (int)min((long long)kL, s.len - (long long)c * kL);
+    by_tokens<true, 2, 2>(y, ex + fy, inv + kQuarter, smem_u32(mats), w, lane);
+    char* vt = st + L::v + w * 16 * L::row + local * 16 * (int)sizeof(T);
     {
-      float dot[16], z[8][4];
+      float dot[4], v[2][4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 be = factor(fac + kBeta * kL, j, lane);
-        const float4 zp = live ? kept.Z[(base * 8 + j) * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int j = 0; j < 2; ++j) {
+        const float2 be = factor(fac + kBeta * kL, w * 16, j, lane), gk = factor(fac + kGK * kL, w * 16, j, lane);
+        const float4 z = j ? z1 : z0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[j][e] = fmaf(y[j][e], sr.inv, x[j][e]);
-        dot[2 * j] = x[j][0] * zp.x + x[j][2] * zp.z;
-        dot[2 * j + 1] = x[j][1] * zp.y + x[j][3] * zp.w;
+        for (int e = 0; e < 4; ++e) x[j][e] += y[j][e];
+        dot[2 * j] = x[j][0] * z.x + x[j][2] * z.z;
+        dot[2 * j + 1] = x[j][1] * z.y + x[j][3] * z.w;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[j][e] *= e & 1 ? be.y : be.x;
+        for (int e = 0; e < 4; ++e) {
+          x[j][e] *= e & 1 ? be.y : be.x;
+          y[j][e] = x[j][e] * (e & 1 ? -gk.y : -gk.x);
+        }
       }
+      give<1, 2>(y, scale_of(tile_max(y)), ex + L::fw, inv + 3 * kQuarter, w, lane);
       const float2 db = column_sum(dot, lane);
-      char* vt = st + L::v + warp * 16 * (int)sizeof(T);
-      const uint32_t vu = su + L::v + warp * 16 * (int)sizeof(T);
-      read_columns<T, L::row>(z, vt, vu, lane);
+      read_columns<T, L::row>(v, vt, lane);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) dot[2 * j + e] = x[j][e] * z[j][e] + x[j][e + 2] * z[j][e + 2];
+        for (int e = 0; e < 2; ++e) dot[2 * j + e] = x[j][e] * v[j][e] + x[j][e + 2] * v[j][e + 2];
       const float2 dv = column_sum(dot, lane);
       if (live) {
-        *reinterpret_cast<float2*>(kept.dbeta + base * kL + 8 * ra + ca) = db;
-        float2* at = reinterpret_cast<float2*>(kept.dots + base * kL + 8 * ra + ca);
-        const float2 was = *at;
-        *at = make_float2(was.x - dv.x, was.y - dv.y);
-      }
-      __syncwarp();
-      T* out = (T*)a.dv + s.b * a.sdv.b + h * a.sdv.h + (s.lo + (long long)c * kL) * a.sdv.t + v0;
-      write_columns<T, L::row>(x, vt, vu, out, a.sdv.t, len, cols, lane);
-    }
-    const Scale sv = scale_of(tile_max<8>(x));
-    if (live) {
-      if (lane == 0) kept.dV_inv[base] = sv.inv;
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        split_a(x[2 * kk], x[2 * kk + 1], sv.mul, hi[kk], lo[kk]);
-        keep(kept.dV + base * NK * 128, kk, lane, hi[kk]);
-        if (NK == 2) keep(kept.dV + (base * NK + 1) * 128, kk, lane, lo[kk]);
+        const size_t at = base * kL + w * 16 + (lane >> 4) * 8 + ca;
+        if ((lane & 12) == 0) {
+          *reinterpret_cast<float2*>(kept.dbeta + at) = db;
+          const float2 was = *reinterpret_cast<const float2*>(kept.dots + at);
+          *reinterpret_cast<float2*>(kept.dots + at) = make_float2(was.x - dv.x, was.y - dv.y);
+        }
+        const Scale sc = scale_of(tile_max(x));
+        uint4 hi, lo;
+        split_a(x[0], x[1], sc.mul, hi, lo);
+        if (lane == 0) kept.dV_inv[base * kQuarter + w] = sc.inv;
+        kept.dV[(base * NK * 4 + w) * 32 + lane] = hi;
+        if (NK == 2) kept.dV[((base * NK + 1) * 4 + w) * 32 + lane] = lo;
       }
     }
+    tile_barrier(local);  // gam dV is in exchange
+    const long long t0 = (long long)c * kL + w * 16;
+    T* out = (T*)a.dv + s.b * a.sdv.b + h * a.sdv.h + (s.lo + t0) * a.sdv.t + v0;
+    write_columns<T, L::row>(x, vt, out, a.sdv.t, (int)max(0LL, min(16LL, s.len - t0)), cols, lane);
     // dS <- gam_63 dS + Q^T (gam dO) - K^T (gam dV)
-    read_columns<T, L::row>(y, dt, du, lane);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 g = factor(fac + kGam * kL, j, lane), qi = factor(fac + kQInv * kL, j, lane);
-      const float2 ki = factor(fac + kKInv * kL, j, lane);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[j][e] *= e & 1 ? g.y * qi.y : g.x * qi.x;
-        x[j][e] *= e & 1 ? -(g.y * ki.y) : -(g.x * ki.x);
-      }
-    }
-    const Scale so = scale_of(tile_max<8>(y)), sx = scale_of(tile_max<8>(x));
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) split_a(y[2 * kk], y[2 * kk + 1], so.mul, hi[kk], lo[kk]);
-    state_add<KP, NP>(D, fac[kGam * kL + kL - 1], hi, lo, so.inv, su + L::q, lane);
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) split_a(x[2 * kk], x[2 * kk + 1], sx.mul, hi[kk], lo[kk]);
-    state_add<KP, NP>(D, 1.f, hi, lo, sx.inv, su, lane);
-    if (L::stages == 1 && c > 0) {
+    to_state<KP, NP>(D, fac[kGam * kL + kL - 1], ex + L::fz, inv + 4 * kQuarter, smem_u32(st) + L::q, w, lane);
+    to_state<KP, NP>(D, 1.f, ex + L::fw, inv + 3 * kQuarter, smem_u32(st), w, lane);
+    if (L::chunks == 1 && c > 0) {
       __syncthreads();
-      fetch_chunk<T, KP, W, true>(a, s, rec - 1, h, c - 1, col0, keys, records, smem_base);
+      fetch_chunk<T, KP, TN, true>(a, s, rec - 1, h, c - 1, col0, keys, records, smem_u32(smem));
+      cp_commit();
     }
   }
   if (a.dS0) {
 #pragma unroll
-    for (int j = 0; j < KP / 8; ++j)
+    for (int j = 0; j < 2 * KS; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int col = ra + (e >> 1) * 8, key = 8 * j + ca + (e & 1);
+        const int col = ra + (e >> 1) * 8, key = w * (KP / 4) + 8 * j + ca + (e & 1);
         if (col < cols && key < a.K) a.dS0[state + (size_t)key * a.V + v0 + col] = D[j][e];
       }
   }
@@ -223,24 +210,28 @@ struct GradStage {
   static constexpr int mats_end = mat + 4 * NP * kTile;
   static constexpr int cols_end = ds + NP * kVB * KP * 2;
   static constexpr int small = cols_end > mats_end ? cols_end : mats_end;
-  // G (64-bit), factors, dO's scales, maxima of the matrices
+  // G in two parts, factors, dO's scales, maxima of the matrices
   static constexpr int bytes = small + kL * 8 + kFactorBytes + kL * 4 + 8 * 4 * 4;
 };
 
-// A kept operand's tiles 4 block .. + 3 as [64 values][COLS] fp16 with one scale, which it returns.
+// A kept operand's tiles first .. first + 3 as [64 values][COLS] fp16 with one scale, which it returns.
 template <int COLS, int NP, int NK>
 __device__ __forceinline__ float load_kept(const uint4* at, const float* inv, size_t base, int first, int tiles, char* out) {
   float big = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (first + i < tiles) big = fmaxf(big, inv[base + first + i]);
+    if (first + i < tiles) {
+      const float4 f = *reinterpret_cast<const float4*>(inv + (base + first + i) * kQuarter);
+      big = fmaxf(big, fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)));
+    }
   constexpr int steps = COLS / 16;
   for (int e = threadIdx.x; e < 4 * NP * steps * 32; e += kGradThreads) {
     const int lane = e & 31, kk = (e >> 5) % steps, part = (e >> 5) / steps % NP, i = (e >> 5) / (steps * NP);
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
     if (first + i < tiles) {
       x = at[(((base + first + i) * NK + part) * steps + kk) * 32 + lane];
-      const __half2 f = __float2half2_rn(inv[base + first + i] / big);  // a power of two, at most 1
+      // a power of two, at most 1
+      const __half2 f = __float2half2_rn(inv[(base + first + i) * kQuarter + kk / (steps / kQuarter)] / big);
       __half2* p = reinterpret_cast<__half2*>(&x);
 #pragma unroll
       for (int j = 0; j < 4; ++j) p[j] = __hmul2(p[j], f);
@@ -290,13 +281,6 @@ __device__ __forceinline__ void gemm(float (&acc)[NT][4], uint32_t at, int pa, i
     }
   }
 }
-template <int NT>
-__device__ __forceinline__ void zero(float (&acc)[NT][4]) {
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-}
 // sum += acc times a factor of the row (the lane's rows r and r + 8)
 template <int NT>
 __device__ __forceinline__ void add_rows(float (&sum)[NT][4], const float (&acc)[NT][4], float f0, float f1) {
@@ -304,6 +288,11 @@ __device__ __forceinline__ void add_rows(float (&sum)[NT][4], const float (&acc)
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[j][e] = fmaf(acc[j][e], e < 2 ? f0 : f1, sum[j][e]);
+}
+
+__device__ __forceinline__ float ends(const Kept& kept, size_t tile) {
+  const float4 e = *reinterpret_cast<const float4*>(kept.ends + tile * kQuarter);
+  return (e.x + e.y) + (e.z + e.w);
 }
 
 // One block for each chunk and key head; the value heads that share it follow one another and their
@@ -314,7 +303,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
   using L = GradStage<T, KP>;
   constexpr int NP = L::NP, NK = kept_parts<T>(), NT = KP / 16;
   extern __shared__ __align__(128) char smem[];
-  double* G = reinterpret_cast<double*>(smem + L::small);
+  float2* G = reinterpret_cast<float2*>(smem + L::small);
   float* fac = reinterpret_cast<float*>(G + kL);
   float* oinv = fac + kFactors * kL;
   float* most = oinv + kL;  // [8 warps][4]
@@ -340,13 +329,13 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
     for (int e = tid; e < kFactors * kL; e += kGradThreads) fac[e] = fin[e];
     if (warp == 0) {
       const double2 g = cumulative(a.g + s.b * a.sg.b + h * a.sg.h, a.sg.t, t0, len, lane);
-      G[2 * lane] = g.x, G[2 * lane + 1] = g.y;
+      G[2 * lane] = two_parts(g.x), G[2 * lane + 1] = two_parts(g.y);
       // dg: what follows in the chunk, and the state's share at its end; dbeta
       float x[2] = {0.f, 0.f}, b[2] = {0.f, 0.f}, end = 0.f;
       for (int i = 0; i < tiles; ++i) {
         const float2 d = *reinterpret_cast<const float2*>(kept.dots + (base + i) * kL + 2 * lane);
         const float2 e = *reinterpret_cast<const float2*>(kept.dbeta + (base + i) * kL + 2 * lane);
-        x[0] += d.x, x[1] += d.y, b[0] += e.x, b[1] += e.y, end += kept.ends[base + i];
+        x[0] += d.x, x[1] += d.y, b[0] += e.x, b[1] += e.y, end += ends(kept, base + i);
       }
       double sum = (double)x[0] + x[1];
 #pragma unroll
@@ -391,7 +380,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
           if (NP == 2) *reinterpret_cast<uint4*>(at + kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
-      cp_wait_all();
+      cp_wait<0>();
       __syncthreads();
       const float o0 = oinv[ra], o1 = oinv[ra + 8];
       float acc[NT][4];
@@ -419,7 +408,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int t = ra + (e >> 1) * 8, q = c0 + j * 8 + ca + (e & 1);
-        const float D = q <= t ? expf((float)(G[t] - G[q])) : 0.f;
+        const float D = q <= t ? decay_between(G[t], G[q]) : 0.f;
         dP[j][e] = q <= t ? dP[j][e] * D : 0.f;
         dW[j][e] = q < t ? dW[j][e] * D : 0.f;
         big[0] = fmaxf(big[0], fabsf(dP[j][e] * fac[kKInv * kL + q]));
@@ -514,28 +503,29 @@ BwdLayout bwd_layout(const GdrArgs& a) {
   };
   l.records = take(nrec * a.H * record_bytes(true));
   l.S = take(st * 2 * key_step);
-  l.S_inv = take(st * 4);
+  l.S_inv = take(st * 16);
   l.Z = take(rt * 4096);
   l.U = take(rt * np * 2048);
-  l.U_inv = take(rt * 4);
+  l.U_inv = take(rt * 16);
   l.dots = take(rt * 256);
   l.D = take(rt * np * key_step);
-  l.D_inv = take(rt * 4);
+  l.D_inv = take(rt * 16);
   l.dV = take(rt * np * 2048);
-  l.dV_inv = take(rt * 4);
+  l.dV_inv = take(rt * 16);
   l.dbeta = take(rt * 256);
-  l.ends = take(rt * 4);
+  l.ends = take(rt * 16);
   l.total = at;
   return l;
 }
 
-template <typename T, int KP, int W>
+template <typename T, int KP, int TN>
 cudaError_t launch_back(const GdrArgs& a, const char* keys, const char* records, const Kept& kept, cudaStream_t stream) {
-  using L = WalkStage<T, KP, W, true>;
-  const auto kernel = gdr_back_kernel<T, KP, W>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::stages * L::bytes);
+  constexpr int smem = Stage<T, KP, TN, true>::bytes;
+  const auto kernel = gdr_back_kernel<T, KP, TN>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3((a.V + 16 * W - 1) / (16 * W), a.H, a.N), 32 * W, L::stages * L::bytes, stream>>>(a, keys, records, kept);
+  const int tiles = (a.V + 15) / 16;
+  kernel<<<dim3((tiles + TN - 1) / TN, a.H, a.N), 32 * kQuarter * TN, smem, stream>>>(a, keys, records, kept);
   return cudaGetLastError();
 }
 
@@ -552,11 +542,10 @@ cudaError_t backward(const GdrArgs& a, char* ws, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_walk<T, KP, true>(a, ws, records, k, stream);
   if (e != cudaSuccess) return e;
-  switch (walk_warps(a)) {
-    case 8: e = launch_back<T, KP, 8>(a, ws, records, k, stream); break;
-    case 4: e = launch_back<T, KP, 4>(a, ws, records, k, stream); break;
-    default: e = launch_back<T, KP, 2>(a, ws, records, k, stream); break;
-  }
+  const int tn = tiles_a_block<T>(a);
+  if constexpr (sizeof(T) == 2)
+    if (tn == 4) e = launch_back<T, KP, 4>(a, ws, records, k, stream);
+  if (tn != 4) e = tn == 2 ? launch_back<T, KP, 2>(a, ws, records, k, stream) : launch_back<T, KP, 1>(a, ws, records, k, stream);
   if (e != cudaSuccess) return e;
   const auto kernel = gdr_grad_kernel<T, KP>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GradStage<T, KP>::bytes);

@@ -172,10 +172,15 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
       const double2 sum = cumulative(g, a.sg.t, t0, len, lane);
       const double last = __shfl_sync(0xffffffffu, sum.y, 31);
       G[t] = two_parts(sum.x), G[t + 1] = two_parts(sum.y);
-      fac[kGam * kL + t] = expf((float)sum.x), fac[kGam * kL + t + 1] = expf((float)sum.y);
-      fac[kW * kL + t] = expf((float)(last - sum.x)), fac[kW * kL + t + 1] = expf((float)(last - sum.y));
-      fac[kBeta * kL + t] = t < len ? be[(t0 + t) * a.sb.t] : 0.f;
-      fac[kBeta * kL + t + 1] = t + 1 < len ? be[(t0 + t + 1) * a.sb.t] : 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const double x = e ? sum.y : sum.x;
+        const float gam = expf((float)x), w = expf((float)(last - x));
+        fac[kGam * kL + t + e] = gam, fac[kW * kL + t + e] = w;
+        fac[kGK * kL + t + e] = gam * fac[kKInv * kL + t + e], fac[kGQ * kL + t + e] = gam * fac[kQInv * kL + t + e];
+        fac[kWK * kL + t + e] = w * fac[kKInv * kL + t + e];
+        fac[kBeta * kL + t + e] = t + e < len ? be[(t0 + t + e) * a.sb.t] : 0.f;
+      }
     }
     __syncthreads();
     // P, rows scaled, and M; blocks above the diagonal are never read

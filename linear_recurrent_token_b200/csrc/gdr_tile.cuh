@@ -19,10 +19,14 @@
 // k, q, R and P and every warp's tile of the state and of the values is scaled so that its largest
 // value lies in [2^14, 2^15), which keeps 22 bits of values down to 2^-17 of it and 11 down to 2^-28.
 //
-// Layout.  A warp owns 16 value columns with the state transposed, S^T [16 x K], in registers as the
-// accumulator of m16n8k16; an accumulator is in the right place to be the next product's A operand,
-// so Z, U and S pass from product to product without leaving the registers.  k, q, R, P are B
-// operands read by ldmatrix from shared memory.
+// Layout.  Four warps own 16 value columns: each has a quarter of the keys of the transposed state
+// S^T [16 x K] in registers, as accumulators of m16n8k16, and a quarter of the chunk's tokens of Z, U and O.
+// An accumulator is in the right place to be the next product's A operand; the four exchange these
+// operands through shared memory, each quarter with its own power of two, and every product of a quarter
+// is summed from zero and scaled on its way into an fp32 sum.  k, q, R and P are B operands, read by
+// ldmatrix.  (One warp with all keys and tokens of its columns was measured first: it needs no
+// exchange, but 255 registers, and with one or two warps to a scheduler the products waited for the
+// splitting between them.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -33,14 +37,16 @@
 namespace mlstm {
 namespace gdr {
 
-constexpr int kL = 64;  // tokens of a chunk
+constexpr int kL = 64;       // tokens of a chunk
+constexpr int kQuarter = 4;  // warps of a tile of 16 value columns
 
 // ---------------------------------------------------------------- a chunk's records in the workspace
 // For each chunk and key head: k and q as [64][KP] fp16, KP = 64 or 128 (zeros behind K and behind the
 // sequence's end), NP parts each.  For each chunk and value head: R (hi, lo) and P (hi, lo where P2) as
 // [64][64] fp16, then the per-token factors.  The 16-byte pieces of a row of these tiles are permuted
 // by the row, so that a record is copied as it is and ldmatrix meets no bank conflicts.
-enum { kGam = 0, kW, kBeta, kKInv, kQInv, kRInv, kPInv, kFactors };
+// kGK = gam / k's scale and so on: what the passes over the chunks multiply by; the rest is for the others.
+enum { kGK = 0, kGQ, kWK, kBeta, kRInv, kPInv, kGam, kW, kKInv, kQInv, kFactors };
 constexpr int kTile = kL * kL * 2;
 constexpr int kFactorBytes = kFactors * kL * 4;
 __host__ __device__ constexpr int keys_bytes(int KP, int np) { return 2 * np * kL * KP * 2; }
@@ -133,7 +139,14 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool i
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {  // all but the last N groups have come
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// the four warps of tile `tile` of the block (barrier 0 is the block's)
+__device__ __forceinline__ void tile_barrier(int tile) {
+  asm volatile("bar.sync %0, %1;" ::"r"(tile + 1), "n"(32 * kQuarter) : "memory");
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -233,12 +246,11 @@ __device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& 
   lo = pack(x - b.x, y - b.y);
 }
 // Two neighbouring accumulator tiles (16 columns) times f as an A operand in two parts.
-__device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], float f, uint32_t (&hi)[4],
-                                        uint32_t (&lo)[4]) {
-  split(c0[0] * f, c0[1] * f, hi[0], lo[0]);
-  split(c0[2] * f, c0[3] * f, hi[1], lo[1]);
-  split(c1[0] * f, c1[1] * f, hi[2], lo[2]);
-  split(c1[2] * f, c1[3] * f, hi[3], lo[3]);
+__device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], float f, uint4& hi, uint4& lo) {
+  split(c0[0] * f, c0[1] * f, hi.x, lo.x);
+  split(c0[2] * f, c0[3] * f, hi.y, lo.y);
+  split(c1[0] * f, c1[1] * f, hi.z, lo.z);
+  split(c1[2] * f, c1[3] * f, hi.w, lo.w);
 }
 template <int N>
 __device__ __forceinline__ float tile_max(const float (&c)[N][4]) {
@@ -248,122 +260,57 @@ __device__ __forceinline__ float tile_max(const float (&c)[N][4]) {
   return warp_max(m);
 }
 
-// acc[j] (j = tokens 8j ..) += A [16 x 16] B, B = columns 16 kk .. of the rows of a [64][KP] tile: one k
-// step of A times the tile's transpose.  NP: parts of B (a plane further on).  lo parts first: they are
-// small, and so is what the tensor cores' sums cut off below them.
-template <int KP, int NP, bool LO_A>
-__device__ __forceinline__ void rows_step(float (&acc)[8][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
-                                          uint32_t tile, int kk, int lane) {
-  const uint32_t at = tile + piece_at<KP>(b_row(lane), kk * 16 + b_col(lane));
-  uint32_t b[4][4];
+// One k step of a product of a quarter: acc (two or more tiles of 8 columns) += A B for NA parts of A and
+// NB of B, the planes of B `plane` bytes apart.  lo parts first: they are small, and so is what the
+// tensor cores' sums cut off below them.  load(tile pair, plane) gives the B fragments.
+template <int NT, int NA, int NB, class Load>
+__device__ __forceinline__ void step(float (&acc)[NT][4], const uint4& ah, const uint4& al, Load load) {
+  const uint32_t hi[4] = {ah.x, ah.y, ah.z, ah.w}, lo[4] = {al.x, al.y, al.z, al.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) ldsm4(b[j], at + j * 16 * KP * 2);
-  if constexpr (LO_A) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) mma(acc[2 * j], lo, b[j][0], b[j][1]), mma(acc[2 * j + 1], lo, b[j][2], b[j][3]);
-  }
-  if constexpr (NP == 2) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < NT; j += 2) {
+    uint32_t b[4];
+    load(b, j, 0);
+    if constexpr (NA == 2) mma(acc[j], lo, b[0], b[1]), mma(acc[j + 1], lo, b[2], b[3]);
+    if constexpr (NB == 2) {
       uint32_t l[4];
-      ldsm4(l, at + kL * KP * 2 + j * 16 * KP * 2);
-      mma(acc[2 * j], hi, l[0], l[1]), mma(acc[2 * j + 1], hi, l[2], l[3]);
+      load(l, j, 1);
+      mma(acc[j], hi, l[0], l[1]), mma(acc[j + 1], hi, l[2], l[3]);
     }
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) mma(acc[2 * j], hi, b[j][0], b[j][1]), mma(acc[2 * j + 1], hi, b[j][2], b[j][3]);
-}
-
-// S = keep S + f A B, A [16 x 64] in two parts, B = a [64][KP] tile: the state's update.  Each product is
-// summed from zero and added in fp32: the tensor cores' sums never run over the state's own bits.
-template <int KP, int NP>
-__device__ __forceinline__ void state_add(float (&S)[KP / 8][4], float keep, const uint32_t (&hi)[4][4],
-                                          const uint32_t (&lo)[4][4], float f, uint32_t tile, int lane) {
-#pragma unroll
-  for (int j = 0; j < KP / 8; j += 4) {
-    float d[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) d[i][e] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      const uint32_t at = tile + kk * 16 * KP * 2;
-      uint32_t b[4], c[4];
-      const int at0 = piece_at<KP>(bt_row(lane), j * 8 + bt_col(lane));
-      const int at1 = piece_at<KP>(bt_row(lane), j * 8 + 16 + bt_col(lane));
-      ldsm4t(b, at + at0);
-      ldsm4t(c, at + at1);
-      mma(d[0], lo[kk], b[0], b[1]), mma(d[1], lo[kk], b[2], b[3]);
-      mma(d[2], lo[kk], c[0], c[1]), mma(d[3], lo[kk], c[2], c[3]);
-      if constexpr (NP == 2) {
-        uint32_t l[4], m[4];
-        ldsm4t(l, at + kL * KP * 2 + at0);
-        ldsm4t(m, at + kL * KP * 2 + at1);
-        mma(d[0], hi[kk], l[0], l[1]), mma(d[1], hi[kk], l[2], l[3]);
-        mma(d[2], hi[kk], m[0], m[1]), mma(d[3], hi[kk], m[2], m[3]);
-      }
-      mma(d[0], hi[kk], b[0], b[1]), mma(d[1], hi[kk], b[2], b[3]);
-      mma(d[2], hi[kk], c[0], c[1]), mma(d[3], hi[kk], c[2], c[3]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[j + i][e] = fmaf(keep, S[j + i][e], f * d[i][e]);
+    mma(acc[j], hi, b[0], b[1]), mma(acc[j + 1], hi, b[2], b[3]);
   }
 }
-
-// acc[j] += sum over k of A[., k] X[t, k] (TRANS: X[k, t]) for a swizzled lower triangular 64 x 64 X:
-// plain, columns k <= t count; transposed, rows k >= t.  NA, NX: parts of A and of X.
-template <bool TRANS, int NA, int NX>
-__device__ __forceinline__ void triangle(float (&acc)[8][4], const uint32_t (&hi)[4][4], const uint32_t (&lo)[4][4],
-                                         uint32_t tile, int lane) {
+template <int NT>
+__device__ __forceinline__ void zero(float (&acc)[NT][4]) {
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk) {
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int jj = TRANS ? 0 : kk; jj < (TRANS ? kk + 1 : 4); ++jj) {  // tokens 16 jj .. + 15 of the result
-      const int row = TRANS ? kk * 16 + bt_row(lane) : jj * 16 + b_row(lane);
-      const int col = TRANS ? jj * 16 + bt_col(lane) : kk * 16 + b_col(lane);
-      const uint32_t at = tile + piece_at<kL>(row, col);
-      uint32_t b[4];
-      if constexpr (TRANS)
-        ldsm4t(b, at);
-      else
-        ldsm4(b, at);
-      if constexpr (NA == 2) mma(acc[2 * jj], lo[kk], b[0], b[1]), mma(acc[2 * jj + 1], lo[kk], b[2], b[3]);
-      if constexpr (NX == 2) {
-        uint32_t l[4];
-        if constexpr (TRANS)
-          ldsm4t(l, at + kTile);
-        else
-          ldsm4(l, at + kTile);
-        mma(acc[2 * jj], hi[kk], l[0], l[1]), mma(acc[2 * jj + 1], hi[kk], l[2], l[3]);
-      }
-      mma(acc[2 * jj], hi[kk], b[0], b[1]), mma(acc[2 * jj + 1], hi[kk], b[2], b[3]);
-    }
-  }
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+}
+template <int NT>
+__device__ __forceinline__ void add_scaled(float (&sum)[NT][4], const float (&x)[NT][4], float f) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[j][e] = fmaf(x[j][e], f, sum[j][e]);
 }
 
-// acc (16 columns x 64 tokens) times f[token] of a factor row
-__device__ __forceinline__ float2 factor(const float* f, int j, int lane) {
-  return *reinterpret_cast<const float2*>(f + 8 * j + 2 * (lane & 3));
+// Factors of the tokens t0 + 8j + 2 (lane & 3) + {0, 1}
+__device__ __forceinline__ float2 factor(const float* f, int t0, int j, int lane) {
+  return *reinterpret_cast<const float2*>(f + t0 + 8 * j + 2 * (lane & 3));
 }
 
-// Sum over the warp's 16 columns of a tile, per token: v[2j + e] holds this lane's share of token
-// 8j + 2 (lane & 3) + e; lane (lane >> 2) = j of the result has the sums of tokens 8j + 2 (lane & 3) + {0, 1}.
-__device__ __forceinline__ float2 column_sum(float (&v)[16], int lane) {
+// Sum over the 16 columns of a quarter's two tiles, per token: v[2j + e] is this lane's share of token
+// 8j + 2 (lane & 3) + e.  Lanes 16 j + (lane & 3) have the sums of tile j's tokens.
+__device__ __forceinline__ float2 column_sum(const float (&v)[4], int lane) {
+  const bool up = lane & 16;
+  float x = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+  float y = (up ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
 #pragma unroll
-  for (int half = 8; half > 1; half /= 2) {
-    // lanes with this bit of j set keep the upper half of the tokens
-    const int bit = half * 2;  // 16, 8, 4: lane bits 4, 3, 2 are bits 2, 1, 0 of lane >> 2
-    const bool up = lane & bit;
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float mine = up ? v[i + half] : v[i], theirs = up ? v[i] : v[i + half];
-      v[i] = mine + __shfl_xor_sync(0xffffffffu, theirs, bit);
-    }
+  for (int d = 8; d > 2; d /= 2) {
+    x += __shfl_xor_sync(0xffffffffu, x, d);
+    y += __shfl_xor_sync(0xffffffffu, y, d);
   }
-  return make_float2(v[0], v[1]);
+  return make_float2(x, y);
 }
 
 }  // namespace gdr

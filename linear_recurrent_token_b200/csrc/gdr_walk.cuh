@@ -7,63 +7,71 @@
 namespace mlstm {
 namespace gdr {
 
-// What the gradients keep of the forward pass, by record of a chunk and value head (states: one more
-// a sequence, the final one) and by tile of 16 value columns.  Operands are stored in the order of the
-// fragments, 512 bytes a warp and step.
+// What the gradients keep of the two passes, by record of a chunk and value head (states: one more a
+// sequence, the final one) and by tile of 16 value columns.  Operands lie as fragments, 512 bytes a k
+// step; each quarter of the steps has its scale.  NK: parts of an operand that only products rounded
+// to the output's type read, one (11 bits) for bf16, two for fp32.
 struct Kept {
   uint4* S;       // S^T at the chunk's start: [state][tile][2 parts][KP / 16][32]
-  float* S_inv;   // the parts' scale: [state][tile]
+  float* S_inv;   // [state][tile][4]
   float4* Z;      // Z': [record][tile][8][32]
-  uint4* U;       // U^T: [record][tile][NK parts][4][32]
-  float* U_inv;   // [record][tile]
+  uint4* U;       // U^T: [record][tile][NK][4][32]
+  float* U_inv;   // [record][tile][4]
   float* dots;    // dO . O, then dO . O - dV . V, over the tile's columns: [record][tile][64]
   // of the pass backward
-  uint4* D;       // dS^T at the chunk's end: [record][tile][NK parts][KP / 16][32]
-  float* D_inv;   // [record][tile]
-  uint4* dV;      // dV^T: [record][tile][NK parts][4][32]
-  float* dV_inv;  // [record][tile]
+  uint4* D;       // dS^T at the chunk's end: [record][tile][NK][KP / 16][32]
+  float* D_inv;   // [record][tile][4]
+  uint4* dV;      // dV^T: [record][tile][NK][4][32]
+  float* dV_inv;  // [record][tile][4]
   float* dbeta;   // dY . Z' over the tile's columns: [record][tile][64]
-  float* ends;    // <dS, S> at the chunk's end over the tile's columns: [record][tile]
+  float* ends;    // <dS, S> at the chunk's end over the tile's columns and a quarter of the keys: [record][tile][4]
 };
-// Parts of an operand that only products rounded to the output's type read: one for bf16 (11 bits).
 template <typename T>
 constexpr int kept_parts() { return sizeof(T) == 4 ? 2 : 1; }
-
-// Four fragment registers of each of `steps` steps as they lie in a warp.
-__device__ __forceinline__ void keep(uint4* at, int step, int lane, const uint32_t (&r)[4]) {
-  at[step * 32 + lane] = make_uint4(r[0], r[1], r[2], r[3]);
-}
 
 template <typename T, int KP, bool P2>
 cudaError_t launch_prep(const GdrArgs& a, char* keys, char* records, cudaStream_t stream);
 
-// bytes of shared memory of one stage: k, q, the columns of v (and dO), the record
-template <typename T, int KP, int W, bool GRAD>
-struct WalkStage {
+// Shared memory of a pass with TN tiles a block: one or two chunks' k, q, columns of v (and dO) and factors,
+// one chunk's R and P, and the tiles' operands in exchange.
+template <typename T, int KP, int TN, bool GRAD>
+struct Stage {
   static constexpr int NP = sizeof(T) == 4 ? 2 : 1;
   static constexpr bool P2 = sizeof(T) == 4 || GRAD;
-  static constexpr int row = 16 * W * (int)sizeof(T) + 16;  // odd multiples of 16 bytes: no bank conflicts
+  static constexpr int row = 16 * TN * (int)sizeof(T) + 16;  // odd multiples of 16 bytes: no bank conflicts
   static constexpr int q = keys_bytes(KP, NP) / 2;
   static constexpr int v = keys_bytes(KP, NP);
   static constexpr int dout = v + kL * row;
-  static constexpr int record = dout + (GRAD ? kL * row : 0);
-  static constexpr int factors = record + (P2 ? 4 : 3) * kTile;
-  static constexpr int bytes = record + record_bytes(P2);
-  static constexpr int stages = 2 * bytes <= 227 * 1024 ? 2 : 1;
+  static constexpr int factors = dout + (GRAD ? kL * row : 0);
+  static constexpr int chunk = factors + kFactorBytes;
+  static constexpr int matrices = record_bytes(P2) - kFactorBytes;
+  // operands in exchange, 512 bytes a k step and part
+  static constexpr int fs = 0;                                 // the state, two parts
+  static constexpr int fu = fs + KP / 16 * 1024;               // U (backward: dO), NU parts
+  static constexpr int nu = P2 ? 2 : 1;
+  static constexpr int fw = fu + 4 * nu * 512;                 // w U (backward: gam dV), two parts
+  static constexpr int fz = fw + 4096;                         // beta Z (backward: gam dO), two parts
+  static constexpr int inv = fz + 4096;                        // scales: [5][4]
+  static constexpr int tile = inv + 5 * kQuarter * 4 + 48;     // a multiple of 128
+  static constexpr int least = chunk + matrices + TN * tile;
+  static constexpr int chunks = least + chunk <= 227 * 1024 ? 2 : 1;
+  static constexpr int bytes = least + (chunks - 1) * chunk;
+  static_assert(tile % 128 == 0, "operands keep their alignment");
+  static_assert(bytes <= 227 * 1024, "a block's shared memory");
 };
 
-// Copies one chunk into a stage: every thread a share, 16 bytes at a time.
-template <typename T, int KP, int W, bool GRAD>
+// Copies the k, q, v, dO and factors of one chunk: every thread a share, 16 bytes at a time.
+template <typename T, int KP, int TN, bool GRAD>
 __device__ __forceinline__ void fetch_chunk(const GdrArgs& a, const Seq& s, long long rec, int h, int c, int col0,
-                                            const char* keys, const char* records, uint32_t stage) {
-  using L = WalkStage<T, KP, W, GRAD>;
+                                            const char* keys, const char* records, uint32_t to) {
+  using L = Stage<T, KP, TN, GRAD>;
   const int tid = threadIdx.x;
-  constexpr int threads = 32 * W;
+  constexpr int threads = 32 * kQuarter * TN;
   const char* k = keys + (rec * a.HK + h / (a.H / a.HK)) * keys_bytes(KP, L::NP);
-  for (int i = tid; i < keys_bytes(KP, L::NP) / 16; i += threads) cp_async16(stage + i * 16, k + i * 16, true);
-  const char* r = records + (rec * a.H + h) * record_bytes(L::P2);
-  for (int i = tid; i < record_bytes(L::P2) / 16; i += threads) cp_async16(stage + L::record + i * 16, r + i * 16, true);
-  constexpr int per = 16 / sizeof(T), pieces = 16 * W / per;  // of a row
+  for (int i = tid; i < keys_bytes(KP, L::NP) / 16; i += threads) cp_async16(to + i * 16, k + i * 16, true);
+  const char* f = records + (rec * a.H + h) * record_bytes(L::P2) + L::matrices;
+  for (int i = tid; i < kFactorBytes / 16; i += threads) cp_async16(to + L::factors + i * 16, f + i * 16, true);
+  constexpr int per = 16 / sizeof(T), pieces = 16 * TN / per;  // of a row
   const long long t0 = (long long)c * kL;
   const T* v = (const T*)a.v + s.b * a.sv.b + h * a.sv.h;
   const T* d = GRAD ? (const T*)a.dout + s.b * a.so.b + h * a.so.h : nullptr;
@@ -71,265 +79,339 @@ __device__ __forceinline__ void fetch_chunk(const GdrArgs& a, const Seq& s, long
     const int row = i / pieces, col = i % pieces * per;
     const bool in = t0 + row < s.len && col0 + col < a.V;
     const long long t = in ? s.lo + t0 + row : 0;
-    cp_async16(stage + L::v + row * L::row + col * (int)sizeof(T), in ? v + t * a.sv.t + col0 + col : v, in);
-    if (GRAD) cp_async16(stage + L::dout + row * L::row + col * (int)sizeof(T), in ? d + t * a.so.t + col0 + col : d, in);
+    cp_async16(to + L::v + row * L::row + col * (int)sizeof(T), in ? v + t * a.sv.t + col0 + col : v, in);
+    if (GRAD) cp_async16(to + L::dout + row * L::row + col * (int)sizeof(T), in ? d + t * a.so.t + col0 + col : d, in);
   }
-  cp_commit();
+}
+// and its R and P
+template <bool P2, int THREADS>
+__device__ __forceinline__ void fetch_matrices(const GdrArgs& a, long long rec, int h, const char* records, uint32_t to) {
+  const char* r = records + (rec * a.H + h) * record_bytes(P2);
+  for (int i = threadIdx.x; i < (record_bytes(P2) - kFactorBytes) / 16; i += THREADS) cp_async16(to + i * 16, r + i * 16, true);
 }
 
-// The warp's 16 columns x 64 tokens of a tile [64][16 W] in shared memory, as an accumulator.
+// A quarter's 16 columns x 16 tokens of a tile [64][16 TN] in shared memory, as accumulator tiles.
 template <typename T, int ROW>
-__device__ __forceinline__ void read_columns(float (&x)[8][4], const char* tile, uint32_t tile_u, int lane) {
+__device__ __forceinline__ void read_columns(float (&x)[2][4], const char* at, int lane) {
   if constexpr (sizeof(T) == 2) {
+    uint32_t r[4];
+    ldsm4t(r, smem_u32(at) + at_row(lane) * ROW + at_col(lane) * 2);
 #pragma unroll
-    for (int jj = 0; jj < 4; ++jj) {
-      uint32_t r[4];
-      ldsm4t(r, tile_u + (jj * 16 + at_row(lane)) * ROW + at_col(lane) * 2);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack_bf16(r[i]);
-        x[2 * jj + (i >> 1)][(i & 1) * 2] = f.x;
-        x[2 * jj + (i >> 1)][(i & 1) * 2 + 1] = f.y;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack_bf16(r[i]);
+      x[i >> 1][(i & 1) * 2] = f.x;
+      x[i >> 1][(i & 1) * 2 + 1] = f.y;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        x[j][e] = *reinterpret_cast<const float*>(tile + (8 * j + 2 * (lane & 3) + (e & 1)) * ROW +
+        x[j][e] = *reinterpret_cast<const float*>(at + (8 * j + 2 * (lane & 3) + (e & 1)) * ROW +
                                                   ((lane >> 2) + (e >> 1) * 8) * 4);
   }
 }
-
-// The inverse, and from there to memory: out points at column col0 of token 0 of the chunk.  The
-// warp's own columns of the tile are free when it calls.
+// The inverse, in the place of what the warp alone has read, and from there to memory: out points at the
+// quarter's first token, of which len are inside, and at the tile's first column, of which cols are.
 template <typename T, int ROW>
-__device__ __forceinline__ void write_columns(const float (&x)[8][4], char* tile, uint32_t tile_u, T* out, long long st,
-                                              int len, int cols, int lane) {
+__device__ __forceinline__ void write_columns(const float (&x)[2][4], char* at, T* out, long long st, int len, int cols,
+                                              int lane) {
+  __syncwarp();
   if constexpr (sizeof(T) == 2) {
-#pragma unroll
-    for (int jj = 0; jj < 4; ++jj)
-      stsm4t(tile_u + (jj * 16 + at_row(lane)) * ROW + at_col(lane) * 2, pack_bf16(x[2 * jj][0], x[2 * jj][1]),
-             pack_bf16(x[2 * jj][2], x[2 * jj][3]), pack_bf16(x[2 * jj + 1][0], x[2 * jj + 1][1]),
-             pack_bf16(x[2 * jj + 1][2], x[2 * jj + 1][3]));
+    stsm4t(smem_u32(at) + at_row(lane) * ROW + at_col(lane) * 2, pack_bf16(x[0][0], x[0][1]), pack_bf16(x[0][2], x[0][3]),
+           pack_bf16(x[1][0], x[1][1]), pack_bf16(x[1][2], x[1][3]));
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<float*>(tile + (8 * j + 2 * (lane & 3) + (e & 1)) * ROW + ((lane >> 2) + (e >> 1) * 8) * 4) =
-            x[j][e];
+        *reinterpret_cast<float*>(at + (8 * j + 2 * (lane & 3) + (e & 1)) * ROW + ((lane >> 2) + (e >> 1) * 8) * 4) = x[j][e];
   }
   __syncwarp();
   constexpr int per = 16 / sizeof(T), pieces = 16 / per;
 #pragma unroll
-  for (int i = 0; i < kL * pieces / 32; ++i) {
+  for (int i = 0; i < 16 * pieces / 32; ++i) {
     const int row = (i * 32 + lane) / pieces, col = (i * 32 + lane) % pieces * per;
     if (row < len && col < cols)
-      *reinterpret_cast<uint4*>(out + row * st + col) = *reinterpret_cast<const uint4*>(tile + row * ROW + col * sizeof(T));
+      *reinterpret_cast<uint4*>(out + row * st + col) = *reinterpret_cast<const uint4*>(at + row * ROW + col * sizeof(T));
   }
 }
 
-// A block takes 16 W value columns of one value head of one sequence.
-template <typename T, int KP, int W, bool GRAD>
-__global__ void __launch_bounds__(32 * W) gdr_walk_kernel(const GdrArgs a, const char* keys, const char* records,
-                                                          const Kept kept) {
-  using L = WalkStage<T, KP, W, GRAD>;
-  constexpr int NP = L::NP;
+// A quarter of an operand into exchange: its k steps (STEPS of them) in two parts, or one, with its scale.
+template <int STEPS, int PARTS>
+__device__ __forceinline__ void give(const float (&x)[2 * STEPS][4], const Scale& sc, char* to, float* inv, int w, int lane) {
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    uint4 hi, lo;
+    split_a(x[2 * i], x[2 * i + 1], sc.mul, hi, lo);
+    uint4* at = reinterpret_cast<uint4*>(to) + (w * STEPS + i) * PARTS * 32 + lane;
+    at[0] = hi;
+    if (PARTS == 2) at[32] = lo;
+  }
+  if (lane == 0) inv[w] = sc.inv;
+}
+template <int PARTS>
+__device__ __forceinline__ void take(const char* from, int k, int lane, uint4& hi, uint4& lo) {
+  const uint4* at = reinterpret_cast<const uint4*>(from) + k * PARTS * 32 + lane;
+  hi = at[0];
+  lo = PARTS == 2 ? at[32] : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// x [16 columns x the quarter's 16 tokens] = F B, F the exchanged state [16 x KP], B = the tokens' rows of the
+// [64][KP] tile k; where TWO, y = F times those of q, which shares F's fragments (one part of F unless LO2).
+template <int KP, int NP, bool TWO, bool LO2>
+__device__ __forceinline__ void by_keys(float (&x)[2][4], float (&y)[2][4], const char* f, const float* inv, uint32_t k,
+                                        uint32_t q, int w, int lane) {
+  constexpr int KS = KP / 16 / kQuarter;
+  zero(x), zero(y);
+#pragma unroll
+  for (int b = 0; b < kQuarter; ++b) {
+    float tx[2][4], ty[2][4];
+    zero(tx), zero(ty);
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      uint4 hi, lo;
+      take<2>(f, b * KS + i, lane, hi, lo);
+      const int at = piece_at<KP>(w * 16 + b_row(lane), (b * KS + i) * 16 + b_col(lane));
+      step<2, 2, NP>(tx, hi, lo, [&](uint32_t (&r)[4], int, int plane) { ldsm4(r, k + at + plane * kL * KP * 2); });
+      if constexpr (TWO)
+        step<2, LO2 ? 2 : 1, NP>(ty, hi, lo, [&](uint32_t (&r)[4], int, int plane) { ldsm4(r, q + at + plane * kL * KP * 2); });
+    }
+    add_scaled(x, tx, inv[b]);
+    if constexpr (TWO) add_scaled(y, ty, inv[b]);
+  }
+}
+
+// sum [16 columns x the quarter's tokens] = F X^T for a lower triangular [64][64] X, F over its columns up to
+// the quarter; TRANS: F X, over its rows from the quarter on.
+template <bool TRANS, int NA, int NX>
+__device__ __forceinline__ void by_tokens(float (&x)[2][4], const char* f, const float* inv, uint32_t tile, int w, int lane) {
+  zero(x);
+#pragma unroll
+  for (int b = 0; b < kQuarter; ++b) {
+    if (TRANS ? b < w : b > w) continue;
+    float t[2][4];
+    zero(t);
+    uint4 hi, lo;
+    take<NA>(f, b, lane, hi, lo);
+    const int at = TRANS ? piece_at<kL>(b * 16 + bt_row(lane), w * 16 + bt_col(lane))
+                         : piece_at<kL>(w * 16 + b_row(lane), b * 16 + b_col(lane));
+    step<2, NA, NX>(t, hi, lo, [&](uint32_t (&r)[4], int, int plane) {
+      if constexpr (TRANS)
+        ldsm4t(r, tile + at + plane * kTile);
+      else
+        ldsm4(r, tile + at + plane * kTile);
+    });
+    add_scaled(x, t, inv[b]);
+  }
+}
+
+// S [16 columns x the quarter's keys] = keep S + F B, F over the 64 tokens, B a [64][KP] tile.
+template <int KP, int NP>
+__device__ __forceinline__ void to_state(float (&S)[KP / 32][4], float keep, const char* f, const float* inv, uint32_t tile,
+                                         int w, int lane) {
+#pragma unroll
+  for (int j = 0; j < KP / 32; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[j][e] *= keep;
+#pragma unroll
+  for (int b = 0; b < kQuarter; ++b) {
+    float d[KP / 32][4];
+    zero(d);
+    uint4 hi, lo;
+    take<2>(f, b, lane, hi, lo);
+    step<KP / 32, 2, NP>(d, hi, lo, [&](uint32_t (&r)[4], int j, int plane) {
+      ldsm4t(r, tile + piece_at<KP>(b * 16 + bt_row(lane), w * (KP / 4) + j * 8 + bt_col(lane)) + plane * kL * KP * 2);
+    });
+    add_scaled(S, d, inv[b]);
+  }
+}
+
+// A block takes 16 TN value columns of one value head of one sequence.
+template <typename T, int KP, int TN, bool GRAD>
+__global__ void __launch_bounds__(32 * kQuarter * TN) gdr_walk_kernel(const GdrArgs a, const char* keys,
+                                                                      const char* records, const Kept kept) {
+  using L = Stage<T, KP, TN, GRAD>;
+  constexpr int NP = L::NP, NK = kept_parts<T>(), KS = KP / 64, threads = 32 * kQuarter * TN;
   constexpr bool FINE = L::P2;  // the output in fp32 accuracy: two parts of S, U and P under it
   extern __shared__ __align__(128) char smem[];
   const int n = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tile = blockIdx.x * W + warp, tiles = (a.V + 15) / 16, col0 = blockIdx.x * 16 * W;
-  const int v0 = tile * 16, cols = min(16, a.V - v0);  // this warp's columns; <= 0 behind the last one
+  const int local = warp / kQuarter, w = warp % kQuarter, tile = blockIdx.x * TN + local, tiles = (a.V + 15) / 16;
+  const int col0 = blockIdx.x * 16 * TN, v0 = tile * 16, cols = min(16, a.V - v0);  // cols <= 0 behind the last
+  const bool live = tile < tiles;
   const Seq s = sequence(a, n);
   const int chunks = (int)((s.len + kL - 1) / kL);
   const size_t state = ((size_t)n * a.H + h) * a.K * a.V;
   const int ra = lane >> 2, ca = 2 * (lane & 3);  // row and first column of this lane in an accumulator
+  char* mats = smem + L::chunks * L::chunk;
+  char* ex = mats + L::matrices + local * L::tile;
+  float* inv = reinterpret_cast<float*>(ex + L::inv);
 
-  float S[KP / 8][4];
+  float S[2 * KS][4];  // keys w KP / 4 ..
 #pragma unroll
-  for (int j = 0; j < KP / 8; ++j)
+  for (int j = 0; j < 2 * KS; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int col = ra + (e >> 1) * 8, key = 8 * j + ca + (e & 1);
+      const int col = ra + (e >> 1) * 8, key = w * (KP / 4) + 8 * j + ca + (e & 1);
       S[j][e] = a.S0 && col < cols && key < a.K ? a.S0[state + (size_t)key * a.V + v0 + col] : 0.f;
     }
-
-  auto keep_state = [&](long long at, const Scale& sc) {  // at: the state's number
+  auto keep_state = [&](long long number, const Scale& sc) {
     if constexpr (GRAD) {
-      if (tile >= tiles) return;
-      const size_t base = ((size_t)at * a.H + h) * tiles + tile;
-      if (lane == 0) kept.S_inv[base] = sc.inv;
+      if (!live) return;
+      const size_t base = ((size_t)number * a.H + h) * tiles + tile;
+      if (lane == 0) kept.S_inv[base * kQuarter + w] = sc.inv;
 #pragma unroll
-      for (int kk = 0; kk < KP / 16; ++kk) {
-        uint32_t hi[4], lo[4];
-        split_a(S[2 * kk], S[2 * kk + 1], sc.mul, hi, lo);
-        keep(kept.S + base * 2 * (KP / 16) * 32, kk, lane, hi);
-        keep(kept.S + (base * 2 + 1) * (KP / 16) * 32, kk, lane, lo);
+      for (int i = 0; i < KS; ++i) {
+        uint4 hi, lo;
+        split_a(S[2 * i], S[2 * i + 1], sc.mul, hi, lo);
+        kept.S[(base * 2 * (KP / 16) + w * KS + i) * 32 + lane] = hi;
+        kept.S[((base * 2 + 1) * (KP / 16) + w * KS + i) * 32 + lane] = lo;
       }
     }
   };
 
-  const uint32_t smem_base = smem_u32(smem);
-  if (chunks > 0) fetch_chunk<T, KP, W, GRAD>(a, s, s.slot, h, 0, col0, keys, records, smem_base);
+  if (chunks > 0) {
+    fetch_chunk<T, KP, TN, GRAD>(a, s, s.slot, h, 0, col0, keys, records, smem_u32(smem));
+    cp_commit();
+  }
   for (int c = 0; c < chunks; ++c) {
     const long long rec = s.slot + c;
-    char* st = smem + (L::stages == 2 ? (c & 1) * L::bytes : 0);
-    const uint32_t su = smem_u32(st);
-    cp_wait_all();
-    __syncthreads();  // the chunk has come, and nobody reads the one before any more
-    if (L::stages == 2 && c + 1 < chunks)
-      fetch_chunk<T, KP, W, GRAD>(a, s, rec + 1, h, c + 1, col0, keys, records, smem_base + ((c + 1) & 1) * L::bytes);
+    const size_t base = ((size_t)rec * a.H + h) * tiles + tile;
+    char* st = smem + (L::chunks == 2 ? (c & 1) * L::chunk : 0);
     const float* fac = reinterpret_cast<const float*>(st + L::factors);
-
-    // X = (K S)^T and (Q S)^T
-    const Scale ss = scale_of(tile_max<KP / 8>(S));
-    keep_state(rec + n, ss);
-    float x[8][4], o[8][4];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[j][e] = o[j][e] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < KP / 16; ++kk) {
-      uint32_t hi[4], lo[4];
-      split_a(S[2 * kk], S[2 * kk + 1], ss.mul, hi, lo);
-      rows_step<KP, NP, true>(x, hi, lo, su, kk, lane);
-      rows_step<KP, NP, FINE>(o, hi, lo, su + L::q, kk, lane);
+    {
+      const Scale sc = scale_of(tile_max(S));
+      give<KS, 2>(S, sc, ex + L::fs, inv, w, lane);
+      keep_state(rec + n, sc);
     }
-    // Z, then Z' = Z + R (beta Z)
-    float z[8][4];
-    char* vt = st + L::v + warp * 16 * (int)sizeof(T);
-    const uint32_t vu = su + L::v + warp * 16 * (int)sizeof(T);
-    read_columns<T, L::row>(z, vt, vu, lane);
-    float zb[8][4];
+    cp_wait<0>();
+    __syncthreads();  // the chunk has come, the states are in exchange, and nobody is in the chunk before
+    fetch_matrices<L::P2, threads>(a, rec, h, records, smem_u32(mats));
+    cp_commit();
+    if (L::chunks == 2) {
+      if (c + 1 < chunks)
+        fetch_chunk<T, KP, TN, GRAD>(a, s, rec + 1, h, c + 1, col0, keys, records, smem_u32(smem) + ((c + 1) & 1) * L::chunk);
+      cp_commit();
+    }
+    // Z = V - gam (K S), O = gam (Q S)
+    float x[2][4], o[2][4], z[2][4], u[2][4];
+    by_keys<KP, NP, true, FINE>(x, o, ex + L::fs, inv, smem_u32(st), smem_u32(st) + L::q, w, lane);
+    char* vt = st + L::v + w * 16 * L::row + local * 16 * (int)sizeof(T);
+    read_columns<T, L::row>(z, vt, lane);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 gam = factor(fac + kGam * kL, j, lane), ki = factor(fac + kKInv * kL, j, lane);
-      const float2 be = factor(fac + kBeta * kL, j, lane), qi = factor(fac + kQInv * kL, j, lane);
+    for (int j = 0; j < 2; ++j) {
+      const float2 gk = factor(fac + kGK * kL, w * 16, j, lane), gq = factor(fac + kGQ * kL, w * 16, j, lane);
+      const float2 be = factor(fac + kBeta * kL, w * 16, j, lane);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float g = e & 1 ? gam.y : gam.x;
-        z[j][e] = fmaf(-g, x[j][e] * ss.inv * (e & 1 ? ki.y : ki.x), z[j][e]);
-        o[j][e] = g * (o[j][e] * ss.inv * (e & 1 ? qi.y : qi.x));
-        zb[j][e] = (e & 1 ? be.y : be.x) * z[j][e];
-        x[j][e] = 0.f;
+        z[j][e] = fmaf(e & 1 ? -gk.y : -gk.x, x[j][e], z[j][e]);
+        o[j][e] *= e & 1 ? gq.y : gq.x;
+        u[j][e] = (e & 1 ? be.y : be.x) * z[j][e];
       }
     }
-    uint32_t hi[4][4], lo[4][4];
-    const Scale sz = scale_of(tile_max<8>(zb));
+    give<1, 2>(u, scale_of(tile_max(u)), ex + L::fz, inv + kQuarter, w, lane);
+    cp_wait<L::chunks == 2 ? 1 : 0>();
+    __syncthreads();  // R and P have come, beta Z is in exchange
+    // Z' = Z + R (beta Z), U = beta Z'
+    by_tokens<false, 2, 2>(x, ex + L::fz, inv + kQuarter, smem_u32(mats), w, lane);
+    float uw[2][4];
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) split_a(zb[2 * kk], zb[2 * kk + 1], sz.mul, hi[kk], lo[kk]);
-    triangle<false, 2, 2>(x, hi, lo, su + L::record, lane);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 ri = factor(fac + kRInv * kL, j, lane), be = factor(fac + kBeta * kL, j, lane);
+    for (int j = 0; j < 2; ++j) {
+      const float2 ri = factor(fac + kRInv * kL, w * 16, j, lane), be = factor(fac + kBeta * kL, w * 16, j, lane);
+      const float2 wk = factor(fac + kWK * kL, w * 16, j, lane);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        z[j][e] = fmaf(x[j][e] * sz.inv, e & 1 ? ri.y : ri.x, z[j][e]);
-        zb[j][e] = (e & 1 ? be.y : be.x) * z[j][e];  // U
-        x[j][e] = 0.f;
+        z[j][e] = fmaf(x[j][e], e & 1 ? ri.y : ri.x, z[j][e]);
+        u[j][e] = (e & 1 ? be.y : be.x) * z[j][e];
+        uw[j][e] = (e & 1 ? wk.y : wk.x) * u[j][e];
       }
     }
-    if constexpr (GRAD) {
-      if (tile < tiles) {
-        float4* at = kept.Z + (((size_t)rec * a.H + h) * tiles + tile) * 8 * 32 + lane;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) at[j * 32] = make_float4(z[j][0], z[j][1], z[j][2], z[j][3]);
-      }
-    }
-    // O = gam (Q S) + P U
-    const Scale su_ = scale_of(tile_max<8>(zb));
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) split_a(zb[2 * kk], zb[2 * kk + 1], su_.mul, hi[kk], lo[kk]);
-    if constexpr (GRAD) {
-      if (tile < tiles) {
-        const size_t base = ((size_t)rec * a.H + h) * tiles + tile;
-        if (lane == 0) kept.U_inv[base] = su_.inv;
-        constexpr int NK = kept_parts<T>();
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          keep(kept.U + base * NK * 128, kk, lane, hi[kk]);
-          if (NK == 2) keep(kept.U + (base * NK + 1) * 128, kk, lane, lo[kk]);
+    {
+      const Scale sc = scale_of(tile_max(u));
+      give<1, L::nu>(u, sc, ex + L::fu, inv + 2 * kQuarter, w, lane);
+      if constexpr (GRAD) {
+        if (live) {
+          kept.Z[(base * 8 + 2 * w) * 32 + lane] = make_float4(z[0][0], z[0][1], z[0][2], z[0][3]);
+          kept.Z[(base * 8 + 2 * w + 1) * 32 + lane] = make_float4(z[1][0], z[1][1], z[1][2], z[1][3]);
+          uint4 hi, lo;
+          split_a(u[0], u[1], sc.mul, hi, lo);
+          if (lane == 0) kept.U_inv[base * kQuarter + w] = sc.inv;
+          kept.U[(base * NK * 4 + w) * 32 + lane] = hi;
+          if (NK == 2) kept.U[((base * NK + 1) * 4 + w) * 32 + lane] = lo;
         }
       }
     }
-    triangle<false, FINE ? 2 : 1, FINE ? 2 : 1>(x, hi, lo, su + L::record + 2 * kTile, lane);
+    give<1, 2>(uw, scale_of(tile_max(uw)), ex + L::fw, inv + 3 * kQuarter, w, lane);
+    tile_barrier(local);  // U and w U are in exchange
+    // O += P U
+    by_tokens<false, L::nu, L::nu>(x, ex + L::fu, inv + 2 * kQuarter, smem_u32(mats) + 2 * kTile, w, lane);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 pi = factor(fac + kPInv * kL, j, lane);
+    for (int j = 0; j < 2; ++j) {
+      const float2 pi = factor(fac + kPInv * kL, w * 16, j, lane);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] = fmaf(x[j][e] * su_.inv, e & 1 ? pi.y : pi.x, o[j][e]);
+      for (int e = 0; e < 4; ++e) o[j][e] = fmaf(x[j][e], e & 1 ? pi.y : pi.x, o[j][e]);
     }
-    const int len = (int)min((long long)kL, s.len - (long long)c * kL);
     if constexpr (GRAD) {
-      float d[8][4], dot[16];
-      read_columns<T, L::row>(d, st + L::dout + warp * 16 * (int)sizeof(T), su + L::dout + warp * 16 * (int)sizeof(T), lane);
+      float d[2][4], dot[4];
+      read_columns<T, L::row>(d, st + L::dout + w * 16 * L::row + local * 16 * (int)sizeof(T), lane);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) dot[2 * j + e] = d[j][e] * o[j][e] + d[j][e + 2] * o[j][e + 2];
       const float2 sum = column_sum(dot, lane);
-      if (tile < tiles)
-        *reinterpret_cast<float2*>(kept.dots + (((size_t)rec * a.H + h) * tiles + tile) * kL + 8 * ra + ca) = sum;
+      if (live && (lane & 12) == 0)
+        *reinterpret_cast<float2*>(kept.dots + base * kL + w * 16 + (lane >> 4) * 8 + ca) = sum;
     } else {
-      T* out = (T*)a.o + s.b * a.so.b + h * a.so.h + (s.lo + (long long)c * kL) * a.so.t + v0;
-      write_columns<T, L::row>(o, vt, vu, out, a.so.t, len, cols, lane);
+      const long long t0 = (long long)c * kL + w * 16;
+      T* out = (T*)a.o + s.b * a.so.b + h * a.so.h + (s.lo + t0) * a.so.t + v0;
+      write_columns<T, L::row>(o, vt, out, a.so.t, (int)max(0LL, min(16LL, s.len - t0)), cols, lane);
     }
     // S <- gam_63 S + (w K)^T U
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 w = factor(fac + kW * kL, j, lane), ki = factor(fac + kKInv * kL, j, lane);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) zb[j][e] *= e & 1 ? w.y * ki.y : w.x * ki.x;
-    }
-    const Scale sw = scale_of(tile_max<8>(zb));
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) split_a(zb[2 * kk], zb[2 * kk + 1], sw.mul, hi[kk], lo[kk]);
-    state_add<KP, NP>(S, fac[kGam * kL + kL - 1], hi, lo, sw.inv, su, lane);
-    if (L::stages == 1 && c + 1 < chunks) {
+    to_state<KP, NP>(S, fac[kGam * kL + kL - 1], ex + L::fw, inv + 3 * kQuarter, smem_u32(st), w, lane);
+    if (L::chunks == 1 && c + 1 < chunks) {
       __syncthreads();
-      fetch_chunk<T, KP, W, GRAD>(a, s, rec + 1, h, c + 1, col0, keys, records, smem_base);
+      fetch_chunk<T, KP, TN, GRAD>(a, s, rec + 1, h, c + 1, col0, keys, records, smem_u32(smem));
+      cp_commit();
     }
   }
-  if constexpr (GRAD) keep_state(s.slot + chunks + n, scale_of(tile_max<KP / 8>(S)));
+  if constexpr (GRAD) keep_state(s.slot + chunks + n, scale_of(tile_max(S)));
   if (a.S_out) {
 #pragma unroll
-    for (int j = 0; j < KP / 8; ++j)
+    for (int j = 0; j < 2 * KS; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int col = ra + (e >> 1) * 8, key = 8 * j + ca + (e & 1);
+        const int col = ra + (e >> 1) * 8, key = w * (KP / 4) + 8 * j + ca + (e & 1);
         if (col < cols && key < a.K) a.S_out[state + (size_t)key * a.V + v0 + col] = S[j][e];
       }
   }
 }
 
-template <typename T, int KP, int W, bool GRAD>
-cudaError_t launch_walk_w(const GdrArgs& a, const char* keys, const char* records, const Kept& kept, cudaStream_t stream) {
-  using L = WalkStage<T, KP, W, GRAD>;
-  const auto kernel = gdr_walk_kernel<T, KP, W, GRAD>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::stages * L::bytes);
-  if (e != cudaSuccess) return e;
-  kernel<<<dim3((a.V + 16 * W - 1) / (16 * W), a.H, a.N), 32 * W, L::stages * L::bytes, stream>>>(a, keys, records, kept);
-  return cudaGetLastError();
+// Tiles a block: as many as fit, fewer while the blocks do not fill the SMs.
+template <typename T>
+int tiles_a_block(const GdrArgs& a) {
+  const long long heads = (long long)a.N * a.H, tiles = (a.V + 15) / 16;
+  if (sizeof(T) == 2 && tiles > 2 && heads * ((tiles + 3) / 4) >= 100) return 4;
+  return tiles > 1 && heads * ((tiles + 1) / 2) >= 100 ? 2 : 1;
 }
 
-// Warps (tiles of 16 columns) a block: more blocks while there are fewer than the SMs.
-inline int walk_warps(const GdrArgs& a) {
-  const long long heads = (long long)a.N * a.H;
-  if (a.V > 64 && heads * ((a.V + 127) / 128) >= 120) return 8;
-  if (a.V > 32 && heads * ((a.V + 63) / 64) >= 100) return 4;
-  return 2;
+template <typename T, int KP, int TN, bool GRAD>
+cudaError_t launch_walk_tn(const GdrArgs& a, const char* keys, const char* records, const Kept& kept, cudaStream_t stream) {
+  constexpr int smem = Stage<T, KP, TN, GRAD>::bytes;
+  const auto kernel = gdr_walk_kernel<T, KP, TN, GRAD>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int tiles = (a.V + 15) / 16;
+  kernel<<<dim3((tiles + TN - 1) / TN, a.H, a.N), 32 * kQuarter * TN, smem, stream>>>(a, keys, records, kept);
+  return cudaGetLastError();
 }
 
 template <typename T, int KP, bool GRAD>
 cudaError_t launch_walk(const GdrArgs& a, const char* keys, const char* records, const Kept& kept, cudaStream_t stream) {
-  switch (walk_warps(a)) {
-    case 8: return launch_walk_w<T, KP, 8, GRAD>(a, keys, records, kept, stream);
-    case 4: return launch_walk_w<T, KP, 4, GRAD>(a, keys, records, kept, stream);
-    default: return launch_walk_w<T, KP, 2, GRAD>(a, keys, records, kept, stream);
-  }
+  const int tn = tiles_a_block<T>(a);
+  if constexpr (sizeof(T) == 2)
+    if (tn == 4) return launch_walk_tn<T, KP, 4, GRAD>(a, keys, records, kept, stream);
+  return tn == 2 ? launch_walk_tn<T, KP, 2, GRAD>(a, keys, records, kept, stream)
+                 : launch_walk_tn<T, KP, 1, GRAD>(a, keys, records, kept, stream);
 }
 
 }  // namespace gdr
