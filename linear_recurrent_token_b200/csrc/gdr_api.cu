@@ -28,6 +28,7 @@ bool strides_ok(mlstm_gdr_stride_t s, long long B, long long H, long long T, int
 
 // distinct elements of [B, H, T, D] lie apart: by ascending stride, each axis steps over those below
 bool apart(mlstm_gdr_stride_t s, long long B, long long H, long long T, long long D) {
+  if (B == 0 || H == 0 || T == 0) return true;
   long long st[3] = {s.b, s.h, s.t}, n[3] = {B, H, T};
   for (int i = 0; i < 3; ++i)
     for (int j = i + 1; j < 3; ++j)

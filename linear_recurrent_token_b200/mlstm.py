@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -167,21 +168,22 @@ def _load(path):
     L.mlstm_bwd.restype = I
     L.mlstm_step.argtypes = [ctypes.POINTER(StepParams)] + [P] * 10 + [P]
     L.mlstm_step.restype = I
-    L.mlstm_gdr_fwd_workspace_size.argtypes = [ctypes.POINTER(GdrParams)]
+    # (parameter structs of these as bytes or by reference)
+    L.mlstm_gdr_fwd_workspace_size.argtypes = [P]
     L.mlstm_gdr_fwd_workspace_size.restype = Z
-    L.mlstm_gdr_fwd.argtypes = [ctypes.POINTER(GdrParams)] + [P] * 10 + [Z, P]
+    L.mlstm_gdr_fwd.argtypes = [P] + [P] * 10 + [Z, P]
     L.mlstm_gdr_fwd.restype = I
-    L.mlstm_gdr_step.argtypes = [ctypes.POINTER(GdrStepParams)] + [P] * 9
+    L.mlstm_gdr_step.argtypes = [P] + [P] * 9
     L.mlstm_gdr_step.restype = I
-    L.mlstm_gdr_bwd_workspace_size.argtypes = [ctypes.POINTER(GdrParams)]
+    L.mlstm_gdr_bwd_workspace_size.argtypes = [P]
     L.mlstm_gdr_bwd_workspace_size.restype = Z
-    L.mlstm_gdr_bwd.argtypes = [ctypes.POINTER(GdrParams)] + [P] * 9 + [GdrStride] * 3 + [P] * 7 + [Z, P]
+    L.mlstm_gdr_bwd.argtypes = [P] + [P] * 9 + [GdrStride] * 3 + [P] * 7 + [Z, P]
     L.mlstm_gdr_bwd.restype = I
-    L.mlstm_rms_norm.argtypes = [ctypes.POINTER(RmsParams)] + [P] * 7
+    L.mlstm_rms_norm.argtypes = [P] + [P] * 7
     L.mlstm_rms_norm.restype = I
-    L.mlstm_rms_norm_bwd_workspace_size.argtypes = [ctypes.POINTER(RmsParams)]
+    L.mlstm_rms_norm_bwd_workspace_size.argtypes = [P]
     L.mlstm_rms_norm_bwd_workspace_size.restype = Z
-    L.mlstm_rms_norm_bwd.argtypes = [ctypes.POINTER(RmsParams)] + [P] * 7 + [Z, P]
+    L.mlstm_rms_norm_bwd.argtypes = [P] + [P] * 7 + [Z, P]
     L.mlstm_rms_norm_bwd.restype = I
     L.mlstm_status_string.argtypes = [I]
     L.mlstm_status_string.restype = ctypes.c_char_p
@@ -542,48 +544,64 @@ def step(q, k, v, igate, fgate, C, n, m, ogate=None, *, num_blocks: int = 1, ret
 
 
 # --------------------------------------------------------------- gated delta rule, root-mean-square norm
+#
+# A decode step's kernel runs for a few microseconds, so these calls keep the host's work down: parameter
+# structs are packed in one go, and the device and the stream are switched only where they have to be.
 
-def _want(name, t, shape, dtype, device, contiguous=False):
+_F32 = torch.float32
+_GDR_PACK = struct.Struct("9i18q")      # GdrParams
+_GDR_STEP_PACK = struct.Struct("7i18q")  # GdrStepParams
+_RMS_PACK = struct.Struct("q4if4x")     # RmsParams
+
+
+def _want(name, t, shape, dtype, device, contiguous=True):
     """Refuses a tensor of another shape, type, layout or device; None passes."""
     if t is None:
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, q (or x) on {device}")
+        raise ValueError(f"{name} is on {t.device}, the first tensor on {device}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _need_cuda(t):
-    if t.device.type != "cuda":
-        raise ValueError(f"the tensors must be on a CUDA device, got {t.device}")
-
-
-def _gdr_stride(name, t, last=True) -> GdrStride:
-    """Strides of [batch, head, token(, width)]; those of axes with one element are never used."""
-    if last and t.shape[-1] > 1 and t.stride(-1) != 1:
+def _strides(name, t, last=True):
+    """Strides of the leading three axes [batch, head, token], the last one contiguous; 0 for those of one
+    element, which are never used."""
+    st, sh = t.stride(), t.shape
+    if last and st[-1] != 1 and sh[-1] > 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
-    return GdrStride(*(t.stride(i) if i < t.dim() - int(last) and t.shape[i] > 1 else 0 for i in range(3)))
+    return (st[0] if sh[0] > 1 else 0, st[1] if sh[1] > 1 else 0, st[2] if sh[2] > 1 else 0)
 
 
-@contextlib.contextmanager
-def _on(device, stream, *tensors):
-    """Makes the device and the stream current, so that what is allocated inside belongs to the stream,
-    and tells the allocator of tensors that come from another one."""
+def _strides2(name, t, last=True):
+    """The same of [batch, head] (no token axis)."""
+    st, sh = t.stride(), t.shape
+    if last and st[-1] != 1 and sh[-1] > 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return (st[0] if sh[0] > 1 else 0, st[1] if sh[1] > 1 else 0, 0)
+
+
+def _on(device, stream, tensors, body):
+    """body(stream pointer) with the device and the stream current, so that what it allocates belongs to the
+    stream; the allocator is told of tensors that come from another one."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, got {device}")
+    if stream is None and device.index == torch._C._cuda_getDevice():  # as torch.cuda.current_device, less wrapping
+        return body(torch._C._cuda_getCurrentRawStream(device.index))
     with torch.cuda.device(device):
         if stream is None or stream == torch.cuda.current_stream():
-            yield _stream_ptr(stream)
-            return
+            return body(torch.cuda.current_stream().cuda_stream)
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
         with torch.cuda.stream(stream):
-            yield _stream_ptr(stream)
+            return body(stream.cuda_stream)
 
 
 def _workspace(workspace, need, device):
@@ -600,28 +618,43 @@ def _gdr_shapes(q, k, v, g, beta, seq_offsets):
     _dtype_code(q)
     B, HK, T, K = q.shape
     H, V = v.shape[1], v.shape[3]
-    _want("k", k, q.shape, q.dtype, q.device)
-    _want("v", v, (B, H, T, V), q.dtype, q.device)
-    _want("g", g, (B, H, T), torch.float32, q.device)
-    _want("beta", beta, (B, H, T), torch.float32, q.device)
+    dt, dev = q.dtype, q.device
+    _want("k", k, q.shape, dt, dev, False)
+    _want("v", v, (B, H, T, V), dt, dev, False)
+    _want("g", g, (B, H, T), _F32, dev, False)
+    _want("beta", beta, (B, H, T), _F32, dev, False)
     N = B
     if seq_offsets is not None:
         if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2 or B != 1:
             raise ValueError("seq_offsets is [N + 1] with N >= 1, and packed tensors have one batch row")
-        _want("seq_offsets", seq_offsets, seq_offsets.shape, torch.int32, q.device, contiguous=True)
+        _want("seq_offsets", seq_offsets, seq_offsets.shape, torch.int32, dev)
         N = seq_offsets.shape[0] - 1
     return B, HK, H, T, K, V, N
 
 
-def gdr_params(q, k, v, g, beta, o=None, seq_offsets=None, mode: str = "auto") -> GdrParams:
-    """Sizes and strides of a call; o: the output, or the gradient of it (None: dense like v's shape)."""
-    B, HK, H, T, K, V, N = _gdr_shapes(q, k, v, g, beta, seq_offsets)
+def _gdr_inputs(q, k, v, g, beta):
+    return _strides("q", q) + _strides("k", k) + _strides("v", v) + _strides("g", g, False) \
+        + _strides("beta", beta, False)
+
+
+def _gdr_pack(sizes, num_seqs, dtype, mode, inputs, so):
+    B, HK, H, T, K, V, _ = sizes
+    return _GDR_PACK.pack(B, HK, H, T, K, V, num_seqs, _DTYPES[dtype], mode, *inputs, *so)
+
+
+def _gdr_mode(mode):
     if mode not in GDR_MODES:
         raise ValueError(f"mode must be one of {tuple(GDR_MODES)}, got {mode!r}")
-    so = GdrStride(H * T * V, T * V, V) if o is None else _gdr_stride("o", o)
-    return GdrParams(B, HK, H, T, K, V, 0 if seq_offsets is None else N, _dtype_code(q), GDR_MODES[mode],
-                     _gdr_stride("q", q), _gdr_stride("k", k), _gdr_stride("v", v), _gdr_stride("g", g, False),
-                     _gdr_stride("beta", beta, False), so)
+    return GDR_MODES[mode]
+
+
+def gdr_params(q, k, v, g, beta, o=None, seq_offsets=None, mode: str = "auto") -> GdrParams:
+    """Sizes and strides of a call; o: the output, or the gradient of it (None: dense like v's shape)."""
+    sizes = _gdr_shapes(q, k, v, g, beta, seq_offsets)
+    B, HK, H, T, K, V, N = sizes
+    so = (H * T * V, T * V, V) if o is None else _strides("o", o)
+    return GdrParams.from_buffer_copy(_gdr_pack(sizes, 0 if seq_offsets is None else N, q.dtype, _gdr_mode(mode),
+                                                _gdr_inputs(q, k, v, g, beta), so))
 
 
 def gdr_fwd_workspace_size(params: GdrParams) -> int:
@@ -646,24 +679,28 @@ def gdr_fwd(q, k, v, g, beta, S0=None, *, seq_offsets=None, mode: str = "auto", 
     seq_offsets [N+1] int32 packs N sequences into one batch row; tokens of no sequence stay as they are
     in a given o and are zero in a new one.  mode "auto", "recurrent" or "chunk".  S_out may be S0.
     Returns (o, S_out)."""
-    B, HK, H, T, K, V, N = _gdr_shapes(q, k, v, g, beta, seq_offsets)
-    _want("S0", S0, (N, H, K, V), torch.float32, q.device, contiguous=True)
-    _want("S_out", S_out, (N, H, K, V), torch.float32, q.device, contiguous=True)
-    _want("o", o, v.shape, q.dtype, q.device)
-    gdr_params(q, k, v, g, beta, o, seq_offsets, mode)
-    _need_cuda(q)
-    with _on(q.device, stream, q, k, v, g, beta, S0, seq_offsets, o, S_out, workspace) as s:
-        if o is None:
-            o = _like(v, seq_offsets is not None)
-        if return_state and S_out is None:
-            S_out = torch.empty((N, H, K, V), dtype=torch.float32, device=q.device)
-        p = gdr_params(q, k, v, g, beta, o, seq_offsets, mode)
-        workspace, ws_len = _workspace(workspace, gdr_fwd_workspace_size(p), q.device)
-        st = lib().mlstm_gdr_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
-                                 _ptr(seq_offsets), _ptr(o), _ptr(S_out), _ptr(workspace), ctypes.c_size_t(ws_len), s)
-    if st != 0:
-        raise MlstmError(st, "mlstm_gdr_fwd")
-    return o, S_out
+    sizes = _gdr_shapes(q, k, v, g, beta, seq_offsets)
+    B, HK, H, T, K, V, N = sizes
+    dev, states = q.device, (N, H, K, V)
+    _want("S0", S0, states, _F32, dev)
+    _want("S_out", S_out, states, _F32, dev)
+    _want("o", o, v.shape, q.dtype, dev, False)
+    code, inputs = _gdr_mode(mode), _gdr_inputs(q, k, v, g, beta)
+    so = None if o is None else _strides("o", o)
+
+    def body(cs):
+        out = _like(v, seq_offsets is not None) if o is None else o
+        last = torch.empty(states, dtype=_F32, device=dev) if return_state and S_out is None else S_out
+        p = _gdr_pack(sizes, 0 if seq_offsets is None else N, q.dtype, code, inputs, so or _strides("o", out))
+        L = lib()
+        ws, ws_len = _workspace(workspace, L.mlstm_gdr_fwd_workspace_size(p), dev)
+        st = L.mlstm_gdr_fwd(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
+                             _ptr(seq_offsets), out.data_ptr(), _ptr(last), _ptr(ws), ws_len, cs)
+        if st != 0:
+            raise MlstmError(st, "mlstm_gdr_fwd")
+        return out, last
+
+    return _on(dev, stream, (q, k, v, g, beta, S0, seq_offsets, o, S_out, workspace), body)
 
 
 def gdr_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None):
@@ -674,32 +711,28 @@ def gdr_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None):
         raise ValueError("q, k are [B, HK, K], v is [B, H, V] and S is [pool, H, K, V]")
     B, HK, K = q.shape
     H, V = v.shape[1], v.shape[2]
-    code = _dtype_code(q)
-    _want("k", k, q.shape, q.dtype, q.device)
-    _want("v", v, (B, H, V), q.dtype, q.device)
-    _want("g", g, (B, H), torch.float32, q.device)
-    _want("beta", beta, (B, H), torch.float32, q.device)
-    _want("S", S, (S.shape[0], H, K, V), torch.float32, q.device, contiguous=True)
-    _want("slots", slots, (B,), torch.int32, q.device, contiguous=True)
-    _want("o", o, v.shape, q.dtype, q.device)
+    code, dev = _dtype_code(q), q.device
+    _want("k", k, q.shape, q.dtype, dev, False)
+    _want("v", v, (B, H, V), q.dtype, dev, False)
+    _want("g", g, (B, H), _F32, dev, False)
+    _want("beta", beta, (B, H), _F32, dev, False)
+    _want("S", S, (S.shape[0], H, K, V), _F32, dev)
+    _want("slots", slots, (B,), torch.int32, dev)
+    _want("o", o, v.shape, q.dtype, dev, False)
+    inputs = _strides2("q", q) + _strides2("k", k) + _strides2("v", v) + _strides2("g", g, False) \
+        + _strides2("beta", beta, False)
+    so = None if o is None else _strides2("o", o)
 
-    def strides(name, t, last=True):
-        s = _gdr_stride(name, t.unsqueeze(2), last)
-        return GdrStride(s.b, s.h, 0)
+    def body(cs):
+        out = torch.empty_like(v) if o is None else o
+        p = _GDR_STEP_PACK.pack(B, HK, H, K, V, S.shape[0], code, *inputs, *(so or _strides2("o", out)))
+        st = lib().mlstm_gdr_step(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                  _ptr(slots), S.data_ptr(), out.data_ptr(), cs)
+        if st != 0:
+            raise MlstmError(st, "mlstm_gdr_step")
+        return out
 
-    if o is not None:
-        strides("o", o)
-    sq, sk, sv, sg, sb = strides("q", q), strides("k", k), strides("v", v), strides("g", g, False), \
-        strides("beta", beta, False)
-    _need_cuda(q)
-    with _on(q.device, stream, q, k, v, g, beta, S, slots, o) as cs:
-        o = torch.empty_like(v) if o is None else o
-        p = GdrStepParams(B, HK, H, K, V, S.shape[0], code, sq, sk, sv, sg, sb, strides("o", o))
-        st = lib().mlstm_gdr_step(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(slots),
-                                  _ptr(S), _ptr(o), cs)
-    if st != 0:
-        raise MlstmError(st, "mlstm_gdr_step")
-    return o
+    return _on(dev, stream, (q, k, v, g, beta, S, slots, o), body)
 
 
 def gdr_bwd(q, k, v, g, beta, do, S0=None, dS=None, *, seq_offsets=None, workspace=None, stream=None):
@@ -707,28 +740,31 @@ def gdr_bwd(q, k, v, g, beta, do, S0=None, dS=None, *, seq_offsets=None, workspa
     [N,H,K,V] fp32 (the gradient of the final states) or None.  Returns a dict: dq, dk, dv in the inputs'
     type, laid out like them where they fill their memory; dg, dbeta [B,H,T] and dS0 [N,H,K,V] fp32.
     Gradients of tokens that no packed sequence holds are zero."""
-    B, HK, H, T, K, V, N = _gdr_shapes(q, k, v, g, beta, seq_offsets)
-    _want("do", do, v.shape, q.dtype, q.device)
-    _want("S0", S0, (N, H, K, V), torch.float32, q.device, contiguous=True)
-    _want("dS", dS, (N, H, K, V), torch.float32, q.device, contiguous=True)
-    p = gdr_params(q, k, v, g, beta, do, seq_offsets, "auto")
-    _need_cuda(q)
-    with _on(q.device, stream, q, k, v, g, beta, do, S0, dS, seq_offsets, workspace) as cs:
-        packed = seq_offsets is not None
-        f32 = dict(dtype=torch.float32, device=q.device)
+    sizes = _gdr_shapes(q, k, v, g, beta, seq_offsets)
+    B, HK, H, T, K, V, N = sizes
+    dev, states = q.device, (N, H, K, V)
+    _want("do", do, v.shape, q.dtype, dev, False)
+    _want("S0", S0, states, _F32, dev)
+    _want("dS", dS, states, _F32, dev)
+    packed = seq_offsets is not None
+    p = _gdr_pack(sizes, N if packed else 0, q.dtype, 0, _gdr_inputs(q, k, v, g, beta), _strides("do", do))
+
+    def body(cs):
+        new = torch.zeros if packed else torch.empty
         out = {"dq": _like(q, packed), "dk": _like(k, packed), "dv": _like(v, packed),
-               "dg": (torch.zeros if packed else torch.empty)((B, H, T), **f32),
-               "dbeta": (torch.zeros if packed else torch.empty)((B, H, T), **f32),
-               "dS0": torch.empty((N, H, K, V), **f32)}
-        workspace, ws_len = _workspace(workspace, gdr_bwd_workspace_size(p), q.device)
-        st = lib().mlstm_gdr_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
-                                 _ptr(seq_offsets), _ptr(do), _ptr(dS), _gdr_stride("dq", out["dq"]),
-                                 _gdr_stride("dk", out["dk"]), _gdr_stride("dv", out["dv"]), _ptr(out["dq"]),
-                                 _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]),
-                                 _ptr(out["dS0"]), _ptr(workspace), ctypes.c_size_t(ws_len), cs)
-    if st != 0:
-        raise MlstmError(st, "mlstm_gdr_bwd")
-    return out
+               "dg": new((B, H, T), dtype=_F32, device=dev), "dbeta": new((B, H, T), dtype=_F32, device=dev),
+               "dS0": torch.empty(states, dtype=_F32, device=dev)}
+        L = lib()
+        ws, ws_len = _workspace(workspace, L.mlstm_gdr_bwd_workspace_size(p), dev)
+        by = [GdrStride(*_strides(n, out[n])) for n in ("dq", "dk", "dv")]
+        st = L.mlstm_gdr_bwd(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
+                             _ptr(seq_offsets), do.data_ptr(), _ptr(dS), *by, *(x.data_ptr() for x in out.values()),
+                             _ptr(ws), ws_len, cs)
+        if st != 0:
+            raise MlstmError(st, "mlstm_gdr_bwd")
+        return out
+
+    return _on(dev, stream, (q, k, v, g, beta, do, S0, dS, seq_offsets, workspace), body)
 
 
 def _rows(name, t):
@@ -747,35 +783,34 @@ def rms_norm(x, residual=None, weight=None, eps: float = 1e-6, *, quant=None, gr
     (in place).  Returns (y, residual_out, scales [..., groups]); the latter two None where there is no
     residual or no quant."""
     rows, D = _rows("x", x)
-    code = _dtype_code(x)
+    code, dev, shape = _dtype_code(x), x.device, x.shape
     if quant not in RMS_QUANT:
         raise ValueError(f"quant must be one of {tuple(RMS_QUANT)}, got {quant!r}")
     if quant is not None and group not in (0, 128):
         raise ValueError(f"group must be 0 or 128, got {group}")
-    ytype = {None: x.dtype, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}[quant]
-    groups = (-(-D // group) if group else 1,)
-    _want("residual", residual, x.shape, x.dtype, x.device, contiguous=True)
-    _want("weight", weight, (D,), torch.float32, x.device, contiguous=True)
-    _want("residual_out", residual_out, x.shape, x.dtype, x.device, contiguous=True)
-    _want("y", y, x.shape, ytype, x.device, contiguous=True)
-    _want("scales", scales, x.shape[:-1] + groups, torch.float32, x.device, contiguous=True)
+    ytype = x.dtype if quant is None else torch.float8_e4m3fn if quant == "e4m3" else torch.int8
+    sshape = shape[:-1] + (-(-D // group) if group else 1,)
+    _want("residual", residual, shape, x.dtype, dev)
+    _want("weight", weight, (D,), _F32, dev)
+    _want("residual_out", residual_out, shape, x.dtype, dev)
+    _want("y", y, shape, ytype, dev)
+    _want("scales", scales, sshape, _F32, dev)
     if residual is None and residual_out is not None:
         raise ValueError("residual_out without a residual")
     if quant is None and scales is not None:
         raise ValueError("scales without quant")
-    _need_cuda(x)
-    with _on(x.device, stream, x, residual, weight, residual_out, y, scales) as cs:
-        y = torch.empty(x.shape, dtype=ytype, device=x.device) if y is None else y
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty_like(x)
-        if quant is not None and scales is None:
-            scales = torch.empty(x.shape[:-1] + groups, dtype=torch.float32, device=x.device)
-        p = RmsParams(rows, D, code, RMS_QUANT[quant], group if quant else 0, eps)
-        st = lib().mlstm_rms_norm(ctypes.byref(p), _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y),
-                                  _ptr(scales), cs)
-    if st != 0:
-        raise MlstmError(st, "mlstm_rms_norm")
-    return y, residual_out, scales
+    p = _RMS_PACK.pack(rows, D, code, RMS_QUANT[quant], group if quant else 0, eps)
+
+    def body(cs):
+        out = torch.empty(shape, dtype=ytype, device=dev) if y is None else y
+        r = torch.empty_like(x) if residual is not None and residual_out is None else residual_out
+        sc = torch.empty(sshape, dtype=_F32, device=dev) if quant is not None and scales is None else scales
+        st = lib().mlstm_rms_norm(p, x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(r), out.data_ptr(), _ptr(sc), cs)
+        if st != 0:
+            raise MlstmError(st, "mlstm_rms_norm")
+        return out, r, sc
+
+    return _on(dev, stream, (x, residual, weight, residual_out, y, scales), body)
 
 
 def rms_norm_bwd(dy, r, weight=None, eps: float = 1e-6, dresidual=None, *, dx=None, return_dweight: bool = True,
@@ -785,20 +820,22 @@ def rms_norm_bwd(dy, r, weight=None, eps: float = 1e-6, dresidual=None, *, dx=No
     gradient of x and of residual alike, may be dy or dresidual (in place).  Returns (dx, dweight [D] fp32
     or None)."""
     rows, D = _rows("r", r)
-    code = _dtype_code(r)
-    _want("dy", dy, r.shape, r.dtype, r.device, contiguous=True)
-    _want("weight", weight, (D,), torch.float32, r.device, contiguous=True)
-    _want("dresidual", dresidual, r.shape, r.dtype, r.device, contiguous=True)
-    _want("dx", dx, r.shape, r.dtype, r.device, contiguous=True)
-    _need_cuda(r)
-    with _on(r.device, stream, dy, r, weight, dresidual, dx, workspace) as cs:
-        dx = torch.empty_like(r) if dx is None else dx
-        dweight = torch.empty(D, dtype=torch.float32, device=r.device) if return_dweight else None
-        p = RmsParams(rows, D, code, 0, 0, eps)
-        need = int(lib().mlstm_rms_norm_bwd_workspace_size(ctypes.byref(p))) if return_dweight else 0
-        workspace, ws_len = _workspace(workspace, need, r.device)
-        st = lib().mlstm_rms_norm_bwd(ctypes.byref(p), _ptr(dy), _ptr(r), _ptr(weight), _ptr(dresidual), _ptr(dx),
-                                      _ptr(dweight), _ptr(workspace), ctypes.c_size_t(ws_len), cs)
-    if st != 0:
-        raise MlstmError(st, "mlstm_rms_norm_bwd")
-    return dx, dweight
+    code, dev, shape = _dtype_code(r), r.device, r.shape
+    _want("dy", dy, shape, r.dtype, dev)
+    _want("weight", weight, (D,), _F32, dev)
+    _want("dresidual", dresidual, shape, r.dtype, dev)
+    _want("dx", dx, shape, r.dtype, dev)
+    p = _RMS_PACK.pack(rows, D, code, 0, 0, eps)
+
+    def body(cs):
+        out = torch.empty_like(r) if dx is None else dx
+        dw = torch.empty(D, dtype=_F32, device=dev) if return_dweight else None
+        L = lib()
+        ws, ws_len = _workspace(workspace, L.mlstm_rms_norm_bwd_workspace_size(p) if return_dweight else 0, dev)
+        st = L.mlstm_rms_norm_bwd(p, dy.data_ptr(), r.data_ptr(), _ptr(weight), _ptr(dresidual), out.data_ptr(),
+                                  _ptr(dw), _ptr(ws), ws_len, cs)
+        if st != 0:
+            raise MlstmError(st, "mlstm_rms_norm_bwd")
+        return out, dw
+
+    return _on(dev, stream, (dy, r, weight, dresidual, dx, workspace), body)
