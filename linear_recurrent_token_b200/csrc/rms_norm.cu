@@ -21,27 +21,87 @@ constexpr int kThreads = 256;  // block size while rows are narrow
 
 enum { kOut = 0, kE4m3 = 1, kInt8 = 2 };
 
-// VEC consecutive values as fp32; VEC = 1 or 16 bytes of the storage type.
+// VEC consecutive values (VEC = 1, or 16 bytes of the storage type) at p, in device or shared memory, as fp32.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* __restrict__ p, float (&x)[VEC]) {
+__device__ __forceinline__ void load_vec(const T* p, float (&x)[VEC]) {
   if constexpr (VEC == 1) {
     x[0] = io<T>::load(p, 0);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(p));
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
   } else {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(u[i] << 16);
-      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      if constexpr (sizeof(T) == 4) {
+        x[i] = __uint_as_float(u[i]);
+      } else {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
     }
   }
 }
 
+// The rows ahead of the one in work, on their way from HBM: every thread copies its own vectors of NT tensors
+// into slots of shared memory that it alone reads, so that a wait for its own copies is all that a row costs
+// and some 100 KB an SM are in flight whatever the block does.  Odd widths (VEC 1) have no such copies and
+// read from memory.
+template <typename T, int VEC, int NT, int TPR>
+struct Ring {
+  static constexpr int NV = kElems / VEC, BLOCK = TPR > kThreads ? TPR : kThreads;
+  static constexpr int stage = NT * NV * BLOCK * 16;
+  static constexpr int stages = 65536 / stage > 2 ? 65536 / stage : 2;
+  static constexpr bool direct = VEC == 1 || 2 * stage > 200 * 1024;  // the widest fp32 rows do not fit twice
+  static constexpr int bytes = direct ? 0 : stages * stage;
+  const T* src[NT];
+  char* smem;
+  long long rows, stride;
+  int D, t;
+
+  __device__ __forceinline__ char* slot(int turn, int k, int i) const {
+    return smem + (((turn % stages) * NT + k) * NV + i) * BLOCK * 16 + threadIdx.x * 16;
+  }
+  // brings row `row` for turn `turn`
+  __device__ __forceinline__ void fetch(int turn, long long row) const {
+    if constexpr (!direct) {
+      if (row < rows)
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VEC;
+            if (src[k] && c < D) {
+              const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot(turn, k, i));
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src[k] + (size_t)row * D + c) : "memory");
+            }
+          }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  }
+  __device__ __forceinline__ void start(long long row) const {
+    if constexpr (!direct)
+#pragma unroll
+      for (int s = 0; s < stages - 1; ++s) fetch(s, row + s * stride);
+  }
+  __device__ __forceinline__ void wait() const {
+    if constexpr (!direct) asm volatile("cp.async.wait_group %0;" ::"n"(stages - 2) : "memory");
+  }
+  // vector i of tensor k; zeros behind the row's end
+  __device__ __forceinline__ void read(int turn, long long row, int k, int i, float (&x)[VEC]) const {
+    const int c = (i * TPR + t) * VEC;
+    if (row < rows && c < D) {
+      if constexpr (!direct)
+        load_vec<T, VEC>(reinterpret_cast<const T*>(slot(turn, k, i)), x);
+      else
+        load_vec<T, VEC>(src[k] + (size_t)row * D + c, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[e] = 0.f;
+    }
+  }
+};
+
 template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* __restrict__ p, const float (&x)[VEC]) {
+__device__ __forceinline__ void store_vec(T* p, const float (&x)[VEC]) {
   if constexpr (VEC == 1) {
     io<T>::store(p, 0, x[0]);
   } else if constexpr (sizeof(T) == 4) {
@@ -53,7 +113,6 @@ __device__ __forceinline__ void store_vec(T* __restrict__ p, const float (&x)[VE
     *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(b);
   }
 }
-
 template <int VEC>
 __device__ __forceinline__ void load_w(const float* __restrict__ p, float (&x)[VEC]) {
   if constexpr (VEC == 1) {
@@ -67,192 +126,218 @@ __device__ __forceinline__ void load_w(const float* __restrict__ p, float (&x)[V
   }
 }
 
-// Sum over the TPR threads of a row, the same value in each; red: N values a warp.  Every thread
-// of the block calls it.
-template <typename F, int N>
-__device__ __forceinline__ void row_sum(F (&v)[N], int tpr, F (*red)[N]) {
-  for (int d = min(tpr, 32) / 2; d > 0; d /= 2)
+// The TPR threads of a row meet (rows of one warp or less have no barrier).
+template <int TPR>
+__device__ __forceinline__ void row_barrier() {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / TPR), "n"(TPR) : "memory");
+}
+
+// Sums over the TPR threads of a row, the same in each; red: N values a warp, not in use by anyone.
+template <int TPR, typename F, int N>
+__device__ __forceinline__ void row_sum(F (&v)[N], F (*red)[N]) {
+#pragma unroll
+  for (int d = (TPR < 32 ? TPR : 32) / 2; d > 0; d /= 2)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-  if (tpr > 32) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = tpr >> 5, base = warp / nw * nw;
-    __syncthreads();  // red is read by the row before
+  if constexpr (TPR > 32) {
+    constexpr int NW = TPR / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (lane == 0)
 #pragma unroll
       for (int i = 0; i < N; ++i) red[warp][i] = v[i];
-    __syncthreads();
+    row_barrier<TPR>();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      F s = lane < nw ? red[base + lane][i] : F(0);
+      v[i] = red[warp / NW * NW + lane % NW][i];
 #pragma unroll
-      for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
-      v[i] = s;
+      for (int d = NW / 2; d > 0; d /= 2) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
     }
   }
 }
 
+template <int NV, int VEC>
+__device__ __forceinline__ void copy(float (&to)[NV][VEC], const float (&from)[NV][VEC]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) to[i][e] = from[i][e];
+}
+
 // Whether fp32 held the sum of squares: ms = mean(r^2) + eps is neither so large that a square may
-// have overflowed nor so small that the squares have vanished (nor NaN).
+// have overflowed nor so small that the squares have vanished (nor NaN).  The same in a row's threads.
 __device__ __forceinline__ bool in_range(float ms) { return ms > 1e-30f && ms < 1e34f; }
 
-// The rows of the block for which fp32 did not: v becomes r / sqrt(mean(r^2) + eps) from sums in 64
-// bits, which hold the squares of every fp32 value.  Every thread of the block calls it.
-template <int NV, int VEC>
-__device__ __noinline__ double normalise_wide(float (&v)[NV][VEC], float eps, int D, int tpr) {
+// The row for which fp32 did not: v becomes r / sqrt(mean(r^2) + eps) from sums in 64 bits, which hold
+// the squares of every fp32 value.
+template <int TPR, int NV, int VEC>
+__device__ __noinline__ double normalise_wide(float (&v)[NV][VEC], float eps, int D) {
   __shared__ double red[32][1];
   double s[1] = {0.0};
   for (int i = 0; i < NV; ++i)
     for (int e = 0; e < VEC; ++e) s[0] += (double)v[i][e] * v[i][e];
-  row_sum<double, 1>(s, tpr, red);
+  if constexpr (TPR > 32) row_barrier<TPR>();
+  row_sum<TPR, double, 1>(s, red);
   const double inv = 1.0 / sqrt(s[0] / D + eps);
   for (int i = 0; i < NV; ++i)
     for (int e = 0; e < VEC; ++e) v[i][e] = (float)(v[i][e] * inv);
   return inv;
 }
 
-// |x| as an unsigned integer: ordered like |x|, with NaN above infinity, so that a maximum keeps it.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
 // VEC values, already divided by their scale, in 8 bits.  NaN stays NaN in e4m3 and gives -127 as an
 // integer (its scale is NaN).
+__device__ __forceinline__ uint32_t as_int8(float z) { return (uint32_t)__float2int_rn(fminf(fmaxf(z, -127.f), 127.f)); }
 template <int KIND, int VEC>
-__device__ __forceinline__ void to8(const float (&z)[VEC], uint8_t (&q)[VEC]) {
-  if constexpr (KIND == kInt8) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) q[e] = (uint8_t)(int8_t)__float2int_rn(fminf(fmaxf(z[e], -127.f), 127.f));
-  } else if constexpr (VEC == 1) {
-    q[0] = (uint8_t)__nv_cvt_float_to_fp8(z[0], __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ void store8(uint8_t* out, const float (&z)[VEC]) {
+  if constexpr (VEC == 1) {
+    *out = KIND == kInt8 ? (uint8_t)as_int8(z[0]) : (uint8_t)__nv_cvt_float_to_fp8(z[0], __NV_SATFINITE, __NV_E4M3);
   } else {
+    uint32_t q[VEC / 4];
 #pragma unroll
-    for (int e = 0; e < VEC; e += 2) {
-      const uint16_t two = __nv_cvt_float2_to_fp8x2(make_float2(z[e], z[e + 1]), __NV_SATFINITE, __NV_E4M3);
-      q[e] = (uint8_t)two, q[e + 1] = (uint8_t)(two >> 8);
+    for (int e = 0; e < VEC / 4; ++e) {
+      const float *x = z + 4 * e;
+      if constexpr (KIND == kInt8) {
+        q[e] = __byte_perm(__byte_perm(as_int8(x[0]), as_int8(x[1]), 0x0040), __byte_perm(as_int8(x[2]), as_int8(x[3]), 0x0040), 0x5410);
+      } else {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
+        q[e] = lo | hi << 16;
+      }
     }
+    if constexpr (VEC == 8)
+      *reinterpret_cast<uint2*>(out) = make_uint2(q[0], q[1]);
+    else
+      *reinterpret_cast<uint32_t*>(out) = q[0];
   }
 }
 
-// Grid: ceil(rows / rows a block).  group: channels that share a scale (D: the whole row).  A group
-// of 128 is 128 / VEC neighbouring lanes of one warp; odd widths (VEC 1) meet in shared memory.
-template <typename T, int VEC, int KIND, int BLOCK>
-__global__ void __launch_bounds__(BLOCK) rms_norm_kernel(const T* x, const T* res, const float* __restrict__ weight,
-                                                        float eps, T* r_out, void* y, float* __restrict__ scales,
-                                                        long long rows, int D, int tpr, int group) {
-  constexpr int NV = kElems / VEC;
-  __shared__ float red[32][1];
-  __shared__ uint32_t gmax[KIND == kOut ? 1 : 128];
-  const int t = threadIdx.x % tpr, sub = threadIdx.x / tpr;
-  const long long row = (long long)blockIdx.x * (blockDim.x / tpr) + sub;
-  const bool live = row < rows;  // dead rows of the last block still take part in the shuffles
-  const size_t base = live ? (size_t)row * D : 0;
-  float v[NV][VEC];
-  float s[1] = {0.f};
+// The larger magnitude, NaN where either is.
+__device__ __forceinline__ float max_abs(float m, float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(x)));
+  return r;
+}
+
+// A block walks rows blockIdx.x, + gridDim.x, ...: a thread meets the same channels every time, keeps their
+// weights, and has the next row's loads in flight while it reduces this one.  group: channels that share
+// a scale (D: the whole row).  A group of 128 is 128 / VEC neighbouring lanes of one warp; odd widths
+// (VEC 1) meet in shared memory.
+template <typename T, int VEC, int KIND, int TPR>
+__global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads, TPR > kThreads ? 1 : 3)
+    rms_norm_kernel(const T* x, const T* res, const float* __restrict__ weight, float eps, T* r_out, void* y,
+                    float* __restrict__ scales, long long rows, int D, float inv_d, int group) {
+  constexpr int NV = kElems / VEC, BLOCK = TPR > kThreads ? TPR : kThreads, RPB = BLOCK / TPR;
+  __shared__ float red[2][32][1];
+  __shared__ uint32_t gmax[2][KIND == kOut ? 1 : 128];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  extern __shared__ __align__(16) char smem[];
+  float w[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + t) * VEC;
+    const int c = (i * TPR + t) * VEC;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-    if (live && c < D) load_vec<T, VEC>(x + base + c, v[i]);
+    for (int e = 0; e < VEC; ++e) w[i][e] = 1.f;
+    if (weight && c < D) load_w<VEC>(weight + c, w[i]);
   }
-  if (res) {
+  using R = Ring<T, VEC, 2, TPR>;
+  const R ring{{x, res}, smem, rows, (long long)gridDim.x * RPB, D, t};
+  ring.start((long long)blockIdx.x * RPB + sub);
+  int turn = 0;
+  for (long long r0 = (long long)blockIdx.x * RPB; r0 < rows; r0 += ring.stride, ++turn) {
+    const long long row = r0 + sub;
+    const bool live = row < rows;  // dead rows of the last block still take part in the shuffles
+    const size_t base = live ? (size_t)row * D : 0;
+    float v[NV][VEC], s[1] = {0.f};
+    ring.wait();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + t) * VEC;
-      if (live && c < D) {
-        float a[VEC];
-        load_vec<T, VEC>(res + base + c, a);
+      const int c = (i * TPR + t) * VEC;
+      ring.read(turn, row, 0, i, v[i]);
+      if (res) {
+        float add[VEC];
+        ring.read(turn, row, 1, i, add);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[i][e] += a[e];
-        store_vec<T, VEC>(r_out + base + c, v[i]);  // this thread's own elements: r_out may be res
+        for (int e = 0; e < VEC; ++e) v[i][e] += add[e];
+        if (live && c < D) store_vec<T, VEC>(r_out + base + c, v[i]);  // this thread's own: r_out may be res or x
       }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s[0] = fmaf(v[i][e], v[i][e], s[0]);
     }
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) s[0] = fmaf(v[i][e], v[i][e], s[0]);
-  row_sum<float, 1>(s, tpr, red);
-  // the norm reads the sum before it is rounded to the storage type
-  const float ms = s[0] / (float)D + eps;
-  float inv = 1.f / sqrtf(ms);
-  if (__syncthreads_or(!in_range(ms))) {  // a block's rows together: the wide sums meet at barriers
-    normalise_wide<NV, VEC>(v, eps, D, tpr);
-    inv = 1.f;
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + t) * VEC;
-    if (live && c < D) {
-      float w[VEC];
-      if (weight) load_w<VEC>(weight + c, w);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        v[i][e] *= inv;
-        if (weight) v[i][e] *= w[e];
-      }
-      if constexpr (KIND == kOut) store_vec<T, VEC>(reinterpret_cast<T*>(y) + base + c, v[i]);
+    ring.fetch(turn + R::stages - 1, row + (R::stages - 1) * ring.stride);
+    row_sum<TPR, float, 1>(s, red[turn & 1]);
+    // the norm reads the sum before it is rounded to the storage type
+    const float ms = s[0] * inv_d + eps;
+    float inv = rsqrtf(ms);
+    if (!in_range(ms)) {
+      float wide[NV][VEC];  // a copy: v itself stays in registers
+      copy(wide, v);
+      normalise_wide<TPR, NV, VEC>(wide, eps, D);
+      copy(v, wide);
+      inv = 1.f;
     }
-  }
-  if constexpr (KIND != kOut) {
-    constexpr float kTop = KIND == kE4m3 ? 448.f : 127.f;
-    const int ngroups = (D + group - 1) / group;
-    uint32_t m[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      m[i] = 0;
+      const int c = (i * TPR + t) * VEC;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) m[i] = max(m[i], abs_bits(v[i][e]));
+      for (int e = 0; e < VEC; ++e) v[i][e] = v[i][e] * inv * w[i][e];
+      if constexpr (KIND == kOut)
+        if (live && c < D) store_vec<T, VEC>(reinterpret_cast<T*>(y) + base + c, v[i]);
     }
-    if (group == D) {  // one maximum for the row
-#pragma unroll
-      for (int i = 1; i < NV; ++i) m[0] = max(m[0], m[i]);
-      for (int d = min(tpr, 32) / 2; d > 0; d /= 2) m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], d));
-      if (tpr > 32) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = tpr >> 5;
-        if (lane == 0) gmax[warp] = m[0];
-        __syncthreads();
-        m[0] = __reduce_max_sync(0xffffffffu, lane < nw ? gmax[warp / nw * nw + lane] : 0u);
-      }
-#pragma unroll
-      for (int i = 1; i < NV; ++i) m[i] = m[0];
-    } else if constexpr (VEC > 1) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int d = 64 / VEC; d > 0; d /= 2) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
-    } else {  // one row a block: the launcher gives odd widths with groups tpr >= 64
-      for (int i = threadIdx.x; i < ngroups; i += blockDim.x) gmax[i] = 0;
-      __syncthreads();
+    if constexpr (KIND != kOut) {
+      constexpr float kTop = KIND == kE4m3 ? 448.f : 127.f;
+      const int ngroups = group == D ? 1 : (D + 127) / 128;
+      uint32_t m[NV];  // magnitudes as integers: in their order, with NaN above infinity
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = i * tpr + t;
-        if (live && c < D) atomicMax(&gmax[c / group], m[i]);  // a maximum: the order does not matter
+        float big = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) big = (i * TPR + t) * VEC < D ? max_abs(big, v[i][e]) : 0.f;
+        m[i] = __float_as_uint(big);
       }
-      __syncthreads();
+      if (group == D) {  // one maximum for the row
 #pragma unroll
-      for (int i = 0; i < NV; ++i) m[i] = i * tpr + t < D ? gmax[(i * tpr + t) / group] : 0;
-    }
+        for (int i = 1; i < NV; ++i) m[0] = max(m[0], m[i]);
+        m[0] = __reduce_max_sync(0xffffffffu, m[0]);
+        if constexpr (TPR > 32) {
+          constexpr int NW = TPR / 32;
+          const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+          if (lane == 0) gmax[turn & 1][warp] = m[0];
+          row_barrier<TPR>();
+          m[0] = __reduce_max_sync(0xffffffffu, gmax[turn & 1][warp / NW * NW + lane % NW]);
+        }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + t) * VEC;
-      if (live && c < D) {
+        for (int i = 1; i < NV; ++i) m[i] = m[0];
+      } else if constexpr (VEC > 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int d = 64 / VEC; d > 0; d /= 2) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
+      } else {  // one row a block: the launcher gives odd widths with groups TPR >= 256
+        for (int i = threadIdx.x; i < ngroups; i += BLOCK) gmax[turn & 1][i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = i * TPR + t;
+          if (live && c < D) atomicMax(&gmax[turn & 1][c / 128], m[i]);  // a maximum: the order does not matter
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) m[i] = i * TPR + t < D ? gmax[turn & 1][(i * TPR + t) / 128] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + t) * VEC;
         const float amax = __uint_as_float(m[i]);
-        const float scale = m[i] == 0 ? 1.f : amax / kTop;
-        if (c % group == 0) scales[(size_t)row * ngroups + c / group] = scale;
-        // one reciprocal for the group; where it could leave fp32's range the quotient itself
-        const float inv_scale = kTop / amax;
-        const bool tiny = amax < 1e-30f;
-        float z[VEC];
+        // one reciprocal for the group, from a maximum that is in its range
+        const float up = amax < 1e-30f ? 0x1p100f : 1.f, f = m[i] == 0 ? 0.f : __fdividef(kTop, amax * up);
+        if (up != 1.f)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) z[e] = m[i] == 0 ? v[i][e] : tiny ? v[i][e] / scale : v[i][e] * inv_scale;
-        uint8_t q[VEC];
-        to8<KIND, VEC>(z, q);
-        uint8_t* out = reinterpret_cast<uint8_t*>(y) + base + c;
-        if constexpr (VEC == 8) {
-          *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(q);
-        } else if constexpr (VEC == 4) {
-          *reinterpret_cast<uint32_t*>(out) = *reinterpret_cast<const uint32_t*>(q);
-        } else {
-          out[0] = q[0];
+          for (int e = 0; e < VEC; ++e) v[i][e] *= up;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[i][e] *= f;
+        if (live && c < D) {
+          store8<KIND, VEC>(reinterpret_cast<uint8_t*>(y) + base + c, v[i]);
+          if (group == D ? c == 0 : c % 128 == 0)  // groups have 128 channels
+            scales[(size_t)row * ngroups + (group == D ? 0 : c / 128)] = m[i] == 0 ? 1.f : amax * (1.f / kTop);
         }
       }
     }
@@ -261,103 +346,101 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_kernel(const T* x, const T* re
 
 // Gradients.  A block walks rows blockIdx.x, + gridDim.x, ... so that a thread meets the same
 // channels every time and keeps their share of the weight's gradient in registers; part: one row
-// of D sums a block, added up in order by rms_norm_dw_kernel.
-template <typename T, int VEC, int BLOCK>
-__global__ void __launch_bounds__(BLOCK) rms_norm_bwd_kernel(const T* dy, const T* __restrict__ r,
-                                                            const float* __restrict__ weight, float eps, const T* dres,
-                                                            T* dx, float* __restrict__ part, long long rows, int D,
-                                                            int tpr) {
-  constexpr int NV = kElems / VEC;
-  extern __shared__ float sums[];  // [rows a block][D] when a block takes several rows
-  __shared__ float red[32][2];
-  const int t = threadIdx.x % tpr, sub = threadIdx.x / tpr, rpb = blockDim.x / tpr;
-  float dw[NV][VEC];
+// of D sums a block, added up in order by rms_norm_dw_kernel.  The next row is loaded before this one
+// is reduced.
+template <typename T, int VEC, int TPR>
+__global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads, TPR > kThreads ? 1 : 2)
+    rms_norm_bwd_kernel(const T* dy, const T* r, const float* __restrict__ weight, float eps, const T* dres, T* dx,
+                        float* __restrict__ part, long long rows, int D, float inv_d) {
+  constexpr int NV = kElems / VEC, BLOCK = TPR > kThreads ? TPR : kThreads, RPB = BLOCK / TPR;
+  extern __shared__ __align__(16) char smem[];  // the ring; then [rows a block][D] sums where a block takes several rows
+  __shared__ float red[2][32][2];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  float dw[NV][VEC], w[NV][VEC];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * TPR + t) * VEC;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[i][e] = 0.f;
-  for (long long r0 = (long long)blockIdx.x * rpb; r0 < rows; r0 += (long long)gridDim.x * rpb) {
+    for (int e = 0; e < VEC; ++e) dw[i][e] = 0.f, w[i][e] = 1.f;
+    if (weight && c < D) load_w<VEC>(weight + c, w[i]);
+  }
+  using R = Ring<T, VEC, 3, TPR>;
+  const R ring{{r, dy, dres}, smem, rows, (long long)gridDim.x * RPB, D, t};
+  ring.start((long long)blockIdx.x * RPB + sub);
+  int turn = 0;
+  for (long long r0 = (long long)blockIdx.x * RPB; r0 < rows; r0 += ring.stride, ++turn) {
     const long long row = r0 + sub;
     const bool live = row < rows;
     const size_t base = live ? (size_t)row * D : 0;
-    float a[NV][VEC], d[NV][VEC];
-    float s[2] = {0.f, 0.f};
+    float a[NV][VEC], d[NV][VEC], s[2] = {0.f, 0.f};
+    ring.wait();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + t) * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) a[i][e] = d[i][e] = 0.f;
-      if (live && c < D) {
-        load_vec<T, VEC>(r + base + c, a[i]);
-        load_vec<T, VEC>(dy + base + c, d[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + t) * VEC;
-      float w[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] = 1.f;
-      if (weight && c < D) load_w<VEC>(weight + c, w);
+      ring.read(turn, row, 0, i, a[i]);
+      ring.read(turn, row, 1, i, d[i]);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         s[0] = fmaf(a[i][e], a[i][e], s[0]);
-        s[1] = fmaf(a[i][e], d[i][e] * w[e], s[1]);
+        s[1] = fmaf(a[i][e], d[i][e] * w[i][e], s[1]);
       }
     }
-    row_sum<float, 2>(s, tpr, red);
-    const float ms = s[0] / (float)D + eps;
-    float inv = 1.f / sqrtf(ms), scale = inv;  // scale takes r to n = r s where a still holds r
-    float along = s[1] / (float)D * inv;       // mean(w dy n)
-    if (__syncthreads_or(!in_range(ms))) {
-      inv = (float)normalise_wide<NV, VEC>(a, eps, D, tpr);
+    row_sum<TPR, float, 2>(s, red[turn & 1]);
+    const float ms = s[0] * inv_d + eps;
+    float inv = rsqrtf(ms), scale = inv;  // scale takes r to n = r s where a still holds r
+    float along = s[1] * inv_d * inv;     // mean(w dy n)
+    if (!in_range(ms)) {
+      float wide[NV][VEC];  // a copy: a itself stays in registers
+      copy(wide, a);
+      inv = (float)normalise_wide<TPR, NV, VEC>(wide, eps, D);
+      copy(a, wide);
       scale = 1.f;
-      s[1] = 0.f;
+      s[0] = s[1] = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + t) * VEC;
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float w = weight && c < D ? weight[c + e] : 1.f;
-          s[1] = fmaf(a[i][e], d[i][e] * w, s[1]);
-        }
-      }
-      row_sum<float, 2>(s, tpr, red);
-      along = s[1] / (float)D;
+        for (int e = 0; e < VEC; ++e) s[1] = fmaf(a[i][e], d[i][e] * w[i][e], s[1]);
+      if constexpr (TPR > 32) row_barrier<TPR>();  // red is still being read
+      row_sum<TPR, float, 2>(s, red[turn & 1]);
+      along = s[1] * inv_d;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + t) * VEC;
+      const int c = (i * TPR + t) * VEC;
       if (live && c < D) {
-        float w[VEC], out[VEC], add[VEC];
+        float out[VEC], more[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) w[e] = 1.f, add[e] = 0.f;
-        if (weight) load_w<VEC>(weight + c, w);
-        if (dres) load_vec<T, VEC>(dres + base + c, add);
+        for (int e = 0; e < VEC; ++e) more[e] = 0.f;
+        if (dres) ring.read(turn, row, 2, i, more);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const float n = a[i][e] * scale;
-          out[e] = fmaf(inv, d[i][e] * w[e] - n * along, add[e]);
+          out[e] = fmaf(inv, d[i][e] * w[i][e] - n * along, more[e]);
           dw[i][e] = fmaf(d[i][e], n, dw[i][e]);
         }
-        store_vec<T, VEC>(dx + base + c, out);  // dx may be dy or dres: this thread's own elements
+        store_vec<T, VEC>(dx + base + c, out);  // dx may be dy or dres: this thread's own elements, read above
       }
     }
+    ring.fetch(turn + R::stages - 1, row + (R::stages - 1) * ring.stride);
   }
   if (!part) return;
-  float* mine = rpb > 1 ? sums + (size_t)sub * D : part + (size_t)blockIdx.x * D;
+  float* sums = reinterpret_cast<float*>(smem);
+  if (RPB > 1) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+  }
+  float* mine = RPB > 1 ? sums + (size_t)sub * D : part + (size_t)blockIdx.x * D;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + t) * VEC;
+    const int c = (i * TPR + t) * VEC;
     if (c < D)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) mine[c + e] = dw[i][e];
   }
-  if (rpb > 1) {
+  if constexpr (RPB > 1) {
     __syncthreads();
-    for (int c = threadIdx.x; c < D; c += blockDim.x) {
+    for (int c = threadIdx.x; c < D; c += BLOCK) {
       float v = 0.f;
-      for (int i = 0; i < rpb; ++i) v += sums[(size_t)i * D + c];
+      for (int i = 0; i < RPB; ++i) v += sums[(size_t)i * D + c];
       part[(size_t)blockIdx.x * D + c] = v;
     }
   }
@@ -395,14 +478,20 @@ int bwd_blocks(long long rows, int rpb) {
   return (int)(need < 296 ? need : 296);
 }
 
-template <typename T, int VEC, int BLOCK>
-cudaError_t fwd_block(const RmsArgs& a, int tpr, int block, cudaStream_t stream) {
-  const long long rpb = block / tpr;
-  const unsigned grid = (unsigned)((a.rows + rpb - 1) / rpb);
-#define MLSTM_RMS(KIND)                                                                                        \
-  rms_norm_kernel<T, VEC, KIND, BLOCK><<<grid, block, 0, stream>>>((const T*)a.x, (const T*)a.res, a.weight,   \
-                                                                   a.eps, (T*)a.r_out, a.y, a.scales, a.rows, \
-                                                                   a.D, tpr, a.group)
+template <typename T, int VEC, int TPR>
+cudaError_t fwd_rows(const RmsArgs& a, cudaStream_t stream) {
+  constexpr int block = TPR > kThreads ? TPR : kThreads;
+  const long long blocks = (a.rows + block / TPR - 1) / (block / TPR);
+  const unsigned grid = (unsigned)(blocks < 444 ? blocks : 444);  // three blocks for each of 148 SMs
+  constexpr int smem = Ring<T, VEC, 2, TPR>::bytes;
+#define MLSTM_RMS(KIND)                                                                                               \
+  do {                                                                                                                \
+    const auto kernel = rms_norm_kernel<T, VEC, KIND, TPR>;                                                           \
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);            \
+    if (e != cudaSuccess) return e;                                                                                   \
+    kernel<<<grid, block, smem, stream>>>((const T*)a.x, (const T*)a.res, a.weight, a.eps, (T*)a.r_out, a.y, a.scales, \
+                                          a.rows, a.D, 1.f / a.D, a.group);                                           \
+  } while (0)
   if (a.kind == kOut)
     MLSTM_RMS(kOut);
   else if (a.kind == kE4m3)
@@ -413,33 +502,46 @@ cudaError_t fwd_block(const RmsArgs& a, int tpr, int block, cudaStream_t stream)
   return cudaGetLastError();
 }
 
-template <typename T, int VEC>
-cudaError_t fwd_kind(const RmsArgs& a, cudaStream_t stream) {
-  const bool odd_groups = VEC == 1 && a.kind != kOut && a.group < a.D;
-  // groups of 128 channels lie inside one warp: 16 or 32 lanes of a row at least
-  const int tpr = row_threads(a.D, odd_groups ? kThreads : 32);
-  return tpr <= kThreads ? fwd_block<T, VEC, kThreads>(a, tpr, kThreads, stream)
-                         : fwd_block<T, VEC, 1024>(a, tpr, tpr, stream);
-}
-
-template <typename T, int VEC, int BLOCK>
-cudaError_t bwd_block(const RmsArgs& a, int tpr, int block, cudaStream_t stream) {
-  const int rpb = block / tpr, grid = bwd_blocks(a.rows, rpb);
-  const size_t smem = rpb > 1 && a.dweight ? sizeof(float) * rpb * a.D : 0;  // at most 8 rows of 512
-  rms_norm_bwd_kernel<T, VEC, BLOCK><<<grid, block, smem, stream>>>(
-      (const T*)a.dy, (const T*)a.x, a.weight, a.eps, (const T*)a.res, (T*)a.y, a.dweight ? a.part : nullptr, a.rows,
-      a.D, tpr);
-  cudaError_t e = cudaGetLastError();
+template <typename T, int VEC, int TPR>
+cudaError_t bwd_rows(const RmsArgs& a, cudaStream_t stream) {
+  constexpr int block = TPR > kThreads ? TPR : kThreads, rpb = block / TPR;
+  const int grid = bwd_blocks(a.rows, rpb);
+  const size_t sums = rpb > 1 && a.dweight ? sizeof(float) * rpb * a.D : 0;  // at most 8 rows of 512
+  constexpr size_t ring = Ring<T, VEC, 3, TPR>::bytes;
+  const size_t smem = sums > ring ? sums : ring;
+  const auto kernel = rms_norm_bwd_kernel<T, VEC, TPR>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, block, smem, stream>>>((const T*)a.dy, (const T*)a.x, a.weight, a.eps,
+                                                                  (const T*)a.res, (T*)a.y,
+                                                                  a.dweight ? a.part : nullptr, a.rows, a.D,
+                                        1.f / a.D);
+  e = cudaGetLastError();
   if (e != cudaSuccess || !a.dweight) return e;
   rms_norm_dw_kernel<<<(a.D + 31) / 32, dim3(32, 32), 0, stream>>>(a.part, grid, a.D, a.dweight);
   return cudaGetLastError();
 }
 
 template <typename T, int VEC>
-cudaError_t bwd_kind(const RmsArgs& a, cudaStream_t stream) {
-  const int tpr = row_threads(a.D, 32);
-  return tpr <= kThreads ? bwd_block<T, VEC, kThreads>(a, tpr, kThreads, stream)
-                         : bwd_block<T, VEC, 1024>(a, tpr, tpr, stream);
+cudaError_t by_rows(const RmsArgs& a, bool backward, cudaStream_t stream) {
+  // groups of 128 channels lie inside one warp: 16 or 32 lanes of a row; odd widths with groups want
+  // one row a block
+  const bool odd_groups = !backward && VEC == 1 && a.kind != kOut && a.group < a.D;
+  switch (row_threads(a.D, odd_groups ? kThreads : 32)) {
+    case 32: return backward ? bwd_rows<T, VEC, 32>(a, stream) : fwd_rows<T, VEC, 32>(a, stream);
+    case 64: return backward ? bwd_rows<T, VEC, 64>(a, stream) : fwd_rows<T, VEC, 64>(a, stream);
+    case 128: return backward ? bwd_rows<T, VEC, 128>(a, stream) : fwd_rows<T, VEC, 128>(a, stream);
+    case 256: return backward ? bwd_rows<T, VEC, 256>(a, stream) : fwd_rows<T, VEC, 256>(a, stream);
+    case 512: return backward ? bwd_rows<T, VEC, 512>(a, stream) : fwd_rows<T, VEC, 512>(a, stream);
+    default: return backward ? bwd_rows<T, VEC, 1024>(a, stream) : fwd_rows<T, VEC, 1024>(a, stream);
+  }
+}
+
+cudaError_t launch(const RmsArgs& a, bool backward, cudaStream_t stream) {
+  const int vec = vec_of(a.D, a.dtype);
+  if (a.dtype)
+    return vec > 1 ? by_rows<__nv_bfloat16, 8>(a, backward, stream) : by_rows<__nv_bfloat16, 1>(a, backward, stream);
+  return vec > 1 ? by_rows<float, 4>(a, backward, stream) : by_rows<float, 1>(a, backward, stream);
 }
 
 }  // namespace
@@ -451,16 +553,8 @@ size_t rms_norm_bwd_workspace_bytes(long long rows, int D) {
   return sizeof(float) * (size_t)bwd_blocks(rows, tpr < kThreads ? kThreads / tpr : 1) * D;
 }
 
-cudaError_t launch_rms_norm(const RmsArgs& a, cudaStream_t stream) {
-  const int vec = vec_of(a.D, a.dtype);
-  if (a.dtype) return vec > 1 ? fwd_kind<__nv_bfloat16, 8>(a, stream) : fwd_kind<__nv_bfloat16, 1>(a, stream);
-  return vec > 1 ? fwd_kind<float, 4>(a, stream) : fwd_kind<float, 1>(a, stream);
-}
+cudaError_t launch_rms_norm(const RmsArgs& a, cudaStream_t stream) { return launch(a, false, stream); }
 
-cudaError_t launch_rms_norm_bwd(const RmsArgs& a, cudaStream_t stream) {
-  const int vec = vec_of(a.D, a.dtype);
-  if (a.dtype) return vec > 1 ? bwd_kind<__nv_bfloat16, 8>(a, stream) : bwd_kind<__nv_bfloat16, 1>(a, stream);
-  return vec > 1 ? bwd_kind<float, 4>(a, stream) : bwd_kind<float, 1>(a, stream);
-}
+cudaError_t launch_rms_norm_bwd(const RmsArgs& a, cudaStream_t stream) { return launch(a, true, stream); }
 
 }  // namespace mlstm
