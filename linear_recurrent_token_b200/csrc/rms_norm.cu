@@ -49,7 +49,8 @@ template <typename T, int VEC, int NT, int TPR>
 struct Ring {
   static constexpr int NV = kElems / VEC, BLOCK = TPR > kThreads ? TPR : kThreads;
   static constexpr int stage = NT * NV * BLOCK * 16;
-  static constexpr int stages = 65536 / stage > 2 ? 65536 / stage : 2;
+  static constexpr int all = NT == 2 ? 65536 : 98304;  // three blocks an SM forward, two backward
+  static constexpr int stages = all / stage > 2 ? all / stage : 2;
   static constexpr bool direct = VEC == 1 || 2 * stage > 200 * 1024;  // the widest fp32 rows do not fit twice
   static constexpr int bytes = direct ? 0 : stages * stage;
   const T* src[NT];
