@@ -1,9 +1,9 @@
 // Gradients of the gated delta rule (formulas, precision and layouts: gdr_tile.cuh).
 //
-// Four kernels: what does not depend on the state (gdr_prep_kernel), the forward pass again, which keeps
+// Five kernels: what does not depend on the state (gdr_prep_kernel), the forward pass again, which keeps
 // the states (gdr_walk_kernel with GRAD), the pass backward over the chunks with dS in registers, which
 // gives dV and everything that needs fp32 accuracy (gdr_back_kernel), and for all chunks at once the
-// gradients of q and k and of the gates (gdr_grad_kernel):
+// gradients of q and k (gdr_grad_kernel) and of the gates (gdr_gates_kernel):
 //     dQ = gam (dO S^T) + (dP o D) K            dP = dO U^T (lower)   dW = dV U^T (strictly lower)
 //     dK = -gam (dV S^T) + w (U dS^T) + (dP o D)^T Q - (dW o D) K - (dW o D)^T K
 // with S at the chunk's start and dS at its end.
@@ -62,10 +62,12 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
         for (int i = 0; i < KS; ++i) {
           uint4 hi, lo;
           split_a(D[2 * i], D[2 * i + 1], sc.mul, hi, lo);
-          kept.D[(base * NK * (KP / 16) + w * KS + i) * 32 + lane] = hi;
-          if (NK == 2) kept.D[((base * NK + 1) * (KP / 16) + w * KS + i) * 32 + lane] = lo;
-          const uint4 sh = kept.S[(after * 2 * (KP / 16) + w * KS + i) * 32 + lane];
-          const uint4 sl = kept.S[((after * 2 + 1) * (KP / 16) + w * KS + i) * 32 + lane];
+          char* at = kept.D + base * NK * 16 * KP * 2;
+          keep16<KP>(at, (w * KS + i) * 16, hi, lane);
+          if (NK == 2) keep16<KP>(at + 16 * KP * 2, (w * KS + i) * 16, lo, lane);
+          const char* state_at = kept.S + after * 2 * 16 * KP * 2;
+          const uint4 sh = kept16<KP>(state_at, (w * KS + i) * 16, lane);
+          const uint4 sl = kept16<KP>(state_at + 16 * KP * 2, (w * KS + i) * 16, lane);
           const uint32_t h4[4] = {sh.x, sh.y, sh.z, sh.w}, l4[4] = {sl.x, sl.y, sl.z, sl.w};
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -95,6 +97,7 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
     {
       float d[2][4];
       read_columns<T, L::row>(d, st + L::dout + w * 16 * L::row + local * 16 * (int)sizeof(T), lane);
+      if (live) keep_tokens<NK>(kept.dO, kept.dO_inv, base, d, scale_of(tile_max(d)), w, lane);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float2 pi = factor(fac + kPInv * kL, w * 16, j, lane), gq = factor(fac + kGQ * kL, w * 16, j, lane);
@@ -160,12 +163,7 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
           const float2 was = *reinterpret_cast<const float2*>(kept.dots + at);
           *reinterpret_cast<float2*>(kept.dots + at) = make_float2(was.x - dv.x, was.y - dv.y);
         }
-        const Scale sc = scale_of(tile_max(x));
-        uint4 hi, lo;
-        split_a(x[0], x[1], sc.mul, hi, lo);
-        if (lane == 0) kept.dV_inv[base * kQuarter + w] = sc.inv;
-        kept.dV[(base * NK * 4 + w) * 32 + lane] = hi;
-        if (NK == 2) kept.dV[((base * NK + 1) * 4 + w) * 32 + lane] = lo;
+        keep_tokens<NK>(kept.dV, kept.dV_inv, base, x, scale_of(tile_max(x)), w, lane);
       }
     }
     tile_barrier(local);  // gam dV is in exchange
@@ -193,93 +191,54 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
 }
 
 // ---------------------------------------------------------------------------------------------
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 512;
 constexpr int kVB = 64;  // value columns at a time: four kept tiles
 
 template <typename T, int KP>
 struct GradStage {
   static constexpr int NP = sizeof(T) == 4 ? 2 : 1;
-  // behind k and q: dO [64][64], then as [value][token or key]: dV, U, S, dS
-  static constexpr int dout = keys_bytes(KP, NP);
+  // behind k and q, once or twice, as [value][token or key]: dO, dV, U, S, dS
+  static constexpr int cols = keys_bytes(KP, NP);
+  static constexpr int dout = 0;
   static constexpr int dv = dout + NP * kTile;
   static constexpr int u = dv + NP * kTile;
   static constexpr int s = u + NP * kTile;
   static constexpr int ds = s + NP * kVB * KP * 2;
-  // after the value columns, in their place: dP o D by k's and q's scales, dW o D by k's, rows and columns
-  static constexpr int mat = dout;
-  static constexpr int mats_end = mat + 4 * NP * kTile;
-  static constexpr int cols_end = ds + NP * kVB * KP * 2;
-  static constexpr int small = cols_end > mats_end ? cols_end : mats_end;
-  // G in two parts, factors, dO's scales, maxima of the matrices
-  static constexpr int bytes = small + kL * 8 + kFactorBytes + kL * 4 + 8 * 4 * 4;
+  // dP o D by k's and q's scales and dW o D by k's, rows and columns, take the place of a head's last columns
+  static constexpr int mats = 4 * NP * kTile;
+  static constexpr int block = ds + NP * kVB * KP * 2 > mats ? ds + NP * kVB * KP * 2 : mats;
+  // factors; scales of the operands in work as powers of two at most 1: [5][4 tiles][4], and their largest
+  static constexpr int small = kFactorBytes + 5 * 16 * 4 + 8 * 4 + kGradThreads / 32 * 4 * 4;
+  static constexpr int blocks = cols + 2 * block + small <= 227 * 1024 ? 2 : 1;
+  static constexpr int bytes = cols + blocks * block + small;
+  static_assert(bytes <= 227 * 1024, "a block's shared memory");
 };
 
-// A kept operand's tiles first .. first + 3 as [64 values][COLS] fp16 with one scale, which it returns.
-template <int COLS, int NP, int NK>
-__device__ __forceinline__ float load_kept(const uint4* at, const float* inv, size_t base, int first, int tiles, char* out) {
-  float big = 0.f;
+// acc[j] += f A B over one k step: A fragments (16 rows from r0) of a tile [k][row] (K_ROWS) or [row][k] with AC
+// columns, B of a tile [k][n] with BC columns from c0.  f, a power of two at most 1, scales A.  Two parts
+// each where NP is 2 (planes pa and pb bytes further on).
+template <bool FRESH, bool K_ROWS, int AC, int BC, int NP, int NT>
+__device__ __forceinline__ void grad_step(float (&acc)[NT][4], uint32_t at, int pa, int r0, uint32_t bt, int pb, int c0, int kk,
+                                          float f, int lane) {
+  const __half2 f2 = __float2half2_rn(f);
+  uint4 a[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (first + i < tiles) {
-      const float4 f = *reinterpret_cast<const float4*>(inv + (base + first + i) * kQuarter);
-      big = fmaxf(big, fmaxf(fmaxf(f.x, f.y), fmaxf(f.z, f.w)));
-    }
-  constexpr int steps = COLS / 16;
-  for (int e = threadIdx.x; e < 4 * NP * steps * 32; e += kGradThreads) {
-    const int lane = e & 31, kk = (e >> 5) % steps, part = (e >> 5) / steps % NP, i = (e >> 5) / (steps * NP);
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (first + i < tiles) {
-      x = at[(((base + first + i) * NK + part) * steps + kk) * 32 + lane];
-      // a power of two, at most 1
-      const __half2 f = __float2half2_rn(inv[(base + first + i) * kQuarter + kk / (steps / kQuarter)] / big);
-      __half2* p = reinterpret_cast<__half2*>(&x);
+  for (int p = 0; p < NP; ++p) {
+    uint32_t r[4];
+    if constexpr (K_ROWS)
+      ldsm4t(r, at + p * pa + piece_at<AC>(kk * 16 + at_row(lane), r0 + at_col(lane)));
+    else
+      ldsm4(r, at + p * pa + piece_at<AC>(r0 + bt_row(lane), kk * 16 + bt_col(lane)));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = __hmul2(p[j], f);
+    for (int i = 0; i < 4; ++i) {
+      const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&r[i]), f2);
+      r[i] = *reinterpret_cast<const uint32_t*>(&x);
     }
-    const int row = i * 16 + (lane >> 2), col = kk * 16 + 2 * (lane & 3);
-    char* o = out + part * kVB * COLS * 2;
-    *reinterpret_cast<uint32_t*>(o + piece_at<COLS>(row, col) + (col & 7) * 2) = x.x;
-    *reinterpret_cast<uint32_t*>(o + piece_at<COLS>(row + 8, col) + (col & 7) * 2) = x.y;
-    *reinterpret_cast<uint32_t*>(o + piece_at<COLS>(row, col + 8) + (col & 7) * 2) = x.z;
-    *reinterpret_cast<uint32_t*>(o + piece_at<COLS>(row + 8, col + 8) + (col & 7) * 2) = x.w;
+    a[p] = make_uint4(r[0], r[1], r[2], r[3]);
   }
-  return big;
-}
-
-// A fragments (16 rows from r0, 16 columns of k step kk): of a tile [row][k], or of a tile [k][row].
-template <int COLS, bool TRANS>
-__device__ __forceinline__ void a_frag(uint32_t (&f)[4], uint32_t tile, int r0, int kk, int lane) {
-  if constexpr (TRANS)
-    ldsm4t(f, tile + piece_at<COLS>(kk * 16 + at_row(lane), r0 + at_col(lane)));
-  else
-    ldsm4(f, tile + piece_at<COLS>(r0 + bt_row(lane), kk * 16 + bt_col(lane)));
-}
-
-// acc[j] += A B over k steps lo .. hi - 1: B a tile [k][n] with COLS columns, n from c0.  Two parts each
-// where NP is 2 (planes pa and pb bytes further on).
-template <int ACOLS, bool TRANS, int COLS, int NP, int NT>
-__device__ __forceinline__ void gemm(float (&acc)[NT][4], uint32_t at, int pa, int r0, uint32_t bt, int pb, int c0, int lo,
-                                     int hi, int lane) {
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) {
-    if (kk < lo || kk >= hi) continue;
-    uint32_t f[4], g[4];
-    a_frag<ACOLS, TRANS>(f, at, r0, kk, lane);
-    if constexpr (NP == 2) a_frag<ACOLS, TRANS>(g, at + pa, r0, kk, lane);
-#pragma unroll
-    for (int j = 0; j < NT; j += 2) {
-      const int off = piece_at<COLS>(kk * 16 + bt_row(lane), c0 + j * 8 + bt_col(lane));
-      uint32_t b[4];
-      ldsm4t(b, bt + off);
-      if constexpr (NP == 2) {
-        uint32_t l[4];
-        ldsm4t(l, bt + pb + off);
-        mma(acc[j], g, b[0], b[1]), mma(acc[j + 1], g, b[2], b[3]);
-        mma(acc[j], f, l[0], l[1]), mma(acc[j + 1], f, l[2], l[3]);
-      }
-      mma(acc[j], f, b[0], b[1]), mma(acc[j + 1], f, b[2], b[3]);
-    }
-  }
+  step<FRESH, NT, NP, NP>(acc, a[0], a[NP - 1], [&](uint32_t (&r)[4], int j, int plane) {
+    ldsm4t(r, bt + plane * pb + piece_at<BC>(kk * 16 + bt_row(lane), c0 + j * 8 + bt_col(lane)));
+  });
 }
 // sum += acc times a factor of the row (the lane's rows r and r + 8)
 template <int NT>
@@ -290,23 +249,19 @@ __device__ __forceinline__ void add_rows(float (&sum)[NT][4], const float (&acc)
     for (int e = 0; e < 4; ++e) sum[j][e] = fmaf(acc[j][e], e < 2 ? f0 : f1, sum[j][e]);
 }
 
-__device__ __forceinline__ float ends(const Kept& kept, size_t tile) {
-  const float4 e = *reinterpret_cast<const float4*>(kept.ends + tile * kQuarter);
-  return (e.x + e.y) + (e.z + e.w);
-}
-
 // One block for each chunk and key head; the value heads that share it follow one another and their
-// shares add up in registers.  A warp has 16 tokens and half of the keys (or of the other token).
+// shares add up in registers.  Warp (t, n) of 4 x 4 has 16 tokens and a quarter of the keys (or of the other
+// token).  The kept operands come 64 value columns at a time, the next ones while these are in work.
 template <typename T, int KP>
 __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a, const char* keys, const char* records,
                                                                 const Kept kept) {
   using L = GradStage<T, KP>;
-  constexpr int NP = L::NP, NK = kept_parts<T>(), NT = KP / 16;
+  constexpr int NP = L::NP, NK = kept_parts<T>(), NT = KP / 32;
   extern __shared__ __align__(128) char smem[];
-  float2* G = reinterpret_cast<float2*>(smem + L::small);
-  float* fac = reinterpret_cast<float*>(G + kL);
-  float* oinv = fac + kFactors * kL;
-  float* most = oinv + kL;  // [8 warps][4]
+  float* fac = reinterpret_cast<float*>(smem + L::cols + L::blocks * L::block);
+  float* rel = fac + kFactors * kL;  // [operand][tile][quarter]
+  float* top = rel + 5 * 16;
+  float* most = top + 8;  // [16 warps][4]
   int n, c;
   Seq s;
   if (!find_chunk(a, blockIdx.x, &n, &s, &c)) return;
@@ -314,158 +269,162 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
   const long long rec = blockIdx.x, t0 = s.lo + (long long)c * kL;
   const int len = (int)min((long long)kL, s.len - (long long)c * kL);
   const uint32_t su = smem_u32(smem);
-  const int r0 = (warp & 3) * 16, half = warp >> 2, k0 = half * (KP / 2), c0 = half * 32;
+  const int mt = warp & 3, nq = warp >> 2, r0 = mt * 16, k0 = nq * (KP / 4), c0 = nq * 16;
   const int ra = r0 + (lane >> 2), ca = 2 * (lane & 3);
+  const int group = a.H / a.HK, parts = (tiles + 3) / 4, total = group * parts;
 
   const char* kq = keys + (rec * a.HK + hk) * keys_bytes(KP, NP);
   for (int i = tid; i < keys_bytes(KP, NP) / 16; i += kGradThreads) cp_async16(su + i * 16, kq + i * 16, true);
-  cp_commit();
 
-  float dq[NT][4], dk[NT][4];
+  // the columns of step i: value head hk group + i / parts, tiles 4 (i % parts) ..
+  auto fetch = [&](int i) {
+    const int h = hk * group + i / parts, first = i % parts * 4;
+    const size_t base = ((size_t)rec * a.H + h) * tiles + first, sbase = ((size_t)(rec + n) * a.H + h) * tiles + first;
+    const uint32_t to = su + L::cols + (L::blocks == 2 ? (i & 1) * L::block : 0);
+    const int live = min(4, tiles - first);
+    // PARTS: parts in memory, of which NP are read
+    auto operand = [&](const char* from, size_t at, int PARTS, int at_smem, int cols) {
+      const int per = 16 * cols * 2 / 16;  // pieces of a tile's part
+      for (int e = tid; e < 4 * NP * per; e += kGradThreads) {
+        const int x = e % per, part = e / per % NP, tile = e / (per * NP);
+        const bool in = tile < live;
+        cp_async16(to + at_smem + part * kVB * cols * 2 + (tile * per + x) * 16,
+                   from + ((at + (in ? tile : 0)) * PARTS + part) * 16 * cols * 2 + x * 16, in);
+      }
+    };
+    operand(kept.dO, base, NK, L::dout, kL);
+    operand(kept.dV, base, NK, L::dv, kL);
+    operand(kept.U, base, NK, L::u, kL);
+    operand(kept.S, sbase, 2, L::s, KP);
+    operand(kept.D, base, NK, L::ds, KP);
+    cp_commit();
+  };
+
+  float dq[NT][4], dk[NT][4], dP[2][4], dW[2][4];
   zero(dq), zero(dk);
-  for (int h = hk * (a.H / a.HK); h < (hk + 1) * (a.H / a.HK); ++h) {
-    const size_t base = ((size_t)rec * a.H + h) * tiles, sbase = ((size_t)(rec + n) * a.H + h) * tiles;
-    const float* fin = reinterpret_cast<const float*>(records + (rec * a.H + h) * record_bytes(true) + 4 * kTile);
-    for (int e = tid; e < kFactors * kL; e += kGradThreads) fac[e] = fin[e];
-    if (warp == 0) {
-      const double2 g = cumulative(a.g + s.b * a.sg.b + h * a.sg.h, a.sg.t, t0, len, lane);
-      G[2 * lane] = two_parts(g.x), G[2 * lane + 1] = two_parts(g.y);
-      // dg: what follows in the chunk, and the state's share at its end; dbeta
-      float x[2] = {0.f, 0.f}, b[2] = {0.f, 0.f}, end = 0.f;
-      for (int i = 0; i < tiles; ++i) {
-        const float2 d = *reinterpret_cast<const float2*>(kept.dots + (base + i) * kL + 2 * lane);
-        const float2 e = *reinterpret_cast<const float2*>(kept.dbeta + (base + i) * kL + 2 * lane);
-        x[0] += d.x, x[1] += d.y, b[0] += e.x, b[1] += e.y, end += ends(kept, base + i);
-      }
-      double sum = (double)x[0] + x[1];
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const double y = __shfl_down_sync(0xffffffffu, sum, d);
-        if (lane + d < 32) sum += y;
-      }
-      const size_t out = ((size_t)s.b * a.H + h) * a.T + t0 + 2 * lane;
-      if (2 * lane < len) a.dg[out] = (float)(sum + end), a.dbeta[out] = b[0];
-      if (2 * lane + 1 < len) a.dg[out + 1] = (float)(sum - x[0] + end), a.dbeta[out + 1] = b[1];
+  fetch(0);
+  for (int i = 0; i < total; ++i) {
+    const int h = hk * group + i / parts, part = i % parts;
+    cp_wait<0>();
+    __syncthreads();  // these columns have come; the ones before, and a head's matrices and factors, are done with
+    if (L::blocks == 2 && i + 1 < total) fetch(i + 1);
+    if (part == 0) {
+      const float* fin = reinterpret_cast<const float*>(records + (rec * a.H + h) * record_bytes(true) + 4 * kTile);
+      for (int e = tid; e < kFactors * kL; e += kGradThreads) fac[e] = fin[e];
+      zero(dP), zero(dW);
     }
-    float dP[4][4], dW[4][4];
-    zero(dP), zero(dW);
-    for (int vb = 0; vb < a.V; vb += kVB) {
-      if (vb > 0) __syncthreads();  // the columns before are read
-      const float uinv = load_kept<kL, NP, NK>(kept.U, kept.U_inv, base, vb / 16, tiles, smem + L::u);
-      const float vinv = load_kept<kL, NP, NK>(kept.dV, kept.dV_inv, base, vb / 16, tiles, smem + L::dv);
-      const float sinv = load_kept<KP, NP, 2>(kept.S, kept.S_inv, sbase, vb / 16, tiles, smem + L::s);
-      const float dinv = load_kept<KP, NP, NK>(kept.D, kept.D_inv, base, vb / 16, tiles, smem + L::ds);
-      {  // dO, rows scaled: four threads a row
-        const int row = tid >> 2, part = tid & 3;
-        const T* src = (const T*)a.dout + s.b * a.so.b + h * a.so.h + (t0 + row) * a.so.t + vb;
-        float x[2][8], m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int col = part * 16 + i * 8;
-          load8<T>(src + col, row < len && vb + col < a.V, x[i]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[i][e]));
-        }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const Scale sc = scale_of(m);
-        if (part == 0) oinv[row] = sc.inv;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split(x[i][2 * e] * sc.mul, x[i][2 * e + 1] * sc.mul, hi[e], lo[e]);
-          char* at = smem + L::dout + piece_at<kVB>(row, part * 16 + i * 8);
-          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if (NP == 2) *reinterpret_cast<uint4*>(at + kTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-      cp_wait<0>();
-      __syncthreads();
-      const float o0 = oinv[ra], o1 = oinv[ra + 8];
-      float acc[NT][4];
-      zero(acc);  // gam (dO S^T)
-      gemm<kVB, false, KP, NP, NT>(acc, su + L::dout, kTile, r0, su + L::s, kVB * KP * 2, k0, 0, 4, lane);
-      add_rows(dq, acc, fac[kGam * kL + ra] * (o0 * sinv), fac[kGam * kL + ra + 8] * (o1 * sinv));
-      zero(acc);  // -gam (dV S^T)
-      gemm<kL, true, KP, NP, NT>(acc, su + L::dv, kTile, r0, su + L::s, kVB * KP * 2, k0, 0, 4, lane);
-      add_rows(dk, acc, -fac[kGam * kL + ra] * (vinv * sinv), -fac[kGam * kL + ra + 8] * (vinv * sinv));
-      zero(acc);  // w (U dS^T)
-      gemm<kL, true, KP, NP, NT>(acc, su + L::u, kTile, r0, su + L::ds, kVB * KP * 2, k0, 0, 4, lane);
-      add_rows(dk, acc, fac[kW * kL + ra] * (uinv * dinv), fac[kW * kL + ra + 8] * (uinv * dinv));
-      float p4[4][4];
-      zero(p4);
-      gemm<kVB, false, kL, NP, 4>(p4, su + L::dout, kTile, r0, su + L::u, kTile, c0, 0, 4, lane);
-      add_rows(dP, p4, o0 * uinv, o1 * uinv);
-      zero(p4);
-      gemm<kL, true, kL, NP, 4>(p4, su + L::dv, kTile, r0, su + L::u, kTile, c0, 0, 4, lane);
-      add_rows(dW, p4, vinv * uinv, vinv * uinv);
+    if (tid < 5 * 32) {  // a warp an operand: its 16 scales against their largest
+      const float* invs[5] = {kept.dO_inv, kept.dV_inv, kept.U_inv, kept.S_inv, kept.D_inv};
+      const size_t at = ((size_t)(warp == 3 ? rec + n : rec) * a.H + h) * tiles + part * 4 + (lane >> 2);
+      const float x = lane < 16 && part * 4 + (lane >> 2) < tiles ? invs[warp][at * kQuarter + (lane & 3)] : 0.f;
+      const float big = warp_max(x);
+      if (lane < 16) rel[warp * 16 + lane] = big > 0.f ? x / big : 0.f;
+      if (lane == 0) top[warp] = big;
     }
-    // (dP o D), (dW o D) with the scales of the rows that they meet, one power of two a matrix
-    float big[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = ra + (e >> 1) * 8, q = c0 + j * 8 + ca + (e & 1);
-        const float D = q <= t ? decay_between(G[t], G[q]) : 0.f;
-        dP[j][e] = q <= t ? dP[j][e] * D : 0.f;
-        dW[j][e] = q < t ? dW[j][e] * D : 0.f;
-        big[0] = fmaxf(big[0], fabsf(dP[j][e] * fac[kKInv * kL + q]));
-        big[1] = fmaxf(big[1], fabsf(dP[j][e] * fac[kQInv * kL + t]));
-        big[2] = fmaxf(big[2], fabsf(dW[j][e] * fac[kKInv * kL + q]));
-        big[3] = fmaxf(big[3], fabsf(dW[j][e] * fac[kKInv * kL + t]));
-      }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      big[i] = warp_max(big[i]);
-      if (lane == 0) most[warp * 4 + i] = big[i];
-    }
-    __syncthreads();  // the columns are read; the matrices take their place
-    Scale sc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float m = 0.f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) m = fmaxf(m, most[w * 4 + i]);
-      sc[i] = scale_of(m);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int t = ra + r * 8, q = c0 + j * 8 + ca;
-        const float2 ki = *reinterpret_cast<const float2*>(fac + kKInv * kL + q);
-        const float kt = fac[kKInv * kL + t], qt = fac[kQInv * kL + t];
-        const float x = dP[j][2 * r], y = dP[j][2 * r + 1], z = dW[j][2 * r], w = dW[j][2 * r + 1];
-        const float v[4][2] = {{x * ki.x, y * ki.y}, {x * qt, y * qt}, {z * ki.x, w * ki.y}, {z * kt, w * kt}};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t hi, lo;
-          split(v[i][0] * sc[i].mul, v[i][1] * sc[i].mul, hi, lo);
-          char* at = smem + L::mat + i * NP * kTile + piece_at<kL>(t, q) + (q & 7) * 2;
-          *reinterpret_cast<uint32_t*>(at) = hi;
-          if (NP == 2) *reinterpret_cast<uint32_t*>(at + kTile) = lo;
-        }
-      }
     __syncthreads();
-    const int mt = warp & 3;
-    const uint32_t mat = su + L::mat, ku = su, qu = su + keys_bytes(KP, NP) / 2;
-    constexpr int pk = kL * KP * 2;
-    float acc[NT][4];
-    zero(acc);
-    gemm<kL, false, KP, NP, NT>(acc, mat, kTile, r0, ku, pk, k0, 0, mt + 1, lane);
-    add_rows(dq, acc, sc[0].inv, sc[0].inv);
-    zero(acc);
-    gemm<kL, true, KP, NP, NT>(acc, mat + NP * kTile, kTile, r0, qu, pk, k0, mt, 4, lane);
-    add_rows(dk, acc, sc[1].inv, sc[1].inv);
-    zero(acc);
-    gemm<kL, false, KP, NP, NT>(acc, mat + 2 * NP * kTile, kTile, r0, ku, pk, k0, 0, mt + 1, lane);
-    add_rows(dk, acc, -sc[2].inv, -sc[2].inv);
-    zero(acc);
-    gemm<kL, true, KP, NP, NT>(acc, mat + 3 * NP * kTile, kTile, r0, ku, pk, k0, mt, 4, lane);
-    add_rows(dk, acc, -sc[3].inv, -sc[3].inv);
-    __syncthreads();  // factors and matrices belong to the next head
+    const uint32_t st = su + L::cols + (L::blocks == 2 ? (i & 1) * L::block : 0);
+    constexpr int ps = kVB * KP * 2;
+    const float *ro = rel, *rv = rel + 16, *ru = rel + 32, *rs = rel + 48, *rd = rel + 64;
+    float acc[NT][4], p[2][4];
+#define MLSTM_GRAD_OVER_VALUES(ACC, K_ROWS, BC, A, RA, B, PB, C0, RB)                                              \
+  grad_step<true, K_ROWS, kL, BC, NP>(ACC, st + A, kTile, r0, st + B, PB, C0, 0, RA[mt] * RB[nq], lane);           \
+  _Pragma("unroll") for (int kk = 1; kk < 4; ++kk) grad_step<false, K_ROWS, kL, BC, NP>(                           \
+      ACC, st + A, kTile, r0, st + B, PB, C0, kk, RA[kk * 4 + mt] * RB[kk * 4 + nq], lane)
+    MLSTM_GRAD_OVER_VALUES(acc, true, KP, L::dout, ro, L::s, ps, k0, rs);  // gam (dO S^T)
+    {
+      const float f = top[0] * top[3];
+      add_rows(dq, acc, fac[kGam * kL + ra] * f, fac[kGam * kL + ra + 8] * f);
+    }
+    MLSTM_GRAD_OVER_VALUES(acc, true, KP, L::dv, rv, L::s, ps, k0, rs);  // -gam (dV S^T)
+    {
+      const float f = -top[1] * top[3];
+      add_rows(dk, acc, fac[kGam * kL + ra] * f, fac[kGam * kL + ra + 8] * f);
+    }
+    MLSTM_GRAD_OVER_VALUES(acc, true, KP, L::u, ru, L::ds, ps, k0, rd);  // w (U dS^T)
+    {
+      const float f = top[2] * top[4];
+      add_rows(dk, acc, fac[kW * kL + ra] * f, fac[kW * kL + ra + 8] * f);
+    }
+    if (c0 <= r0) {  // the other token's quarter is not behind this one
+      MLSTM_GRAD_OVER_VALUES(p, true, kL, L::dout, ro, L::u, kTile, c0, ru);
+      add_scaled(dP, p, top[0] * top[2]);
+      MLSTM_GRAD_OVER_VALUES(p, true, kL, L::dv, rv, L::u, kTile, c0, ru);
+      add_scaled(dW, p, top[1] * top[2]);
+    }
+#undef MLSTM_GRAD_OVER_VALUES
+    if (part == parts - 1) {
+      // (dP o D), (dW o D) with the scales of the rows that they meet, one power of two a matrix
+      float big[4] = {0.f, 0.f, 0.f, 0.f};
+      const float2* G = reinterpret_cast<const float2*>(fac + kG * kL);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = ra + (e >> 1) * 8, q = c0 + j * 8 + ca + (e & 1);
+          const float D = q <= t ? decay_between(G[t], G[q]) : 0.f;
+          dP[j][e] = q <= t ? dP[j][e] * D : 0.f;
+          dW[j][e] = q < t ? dW[j][e] * D : 0.f;
+          big[0] = fmaxf(big[0], fabsf(dP[j][e] * fac[kKInv * kL + q]));
+          big[1] = fmaxf(big[1], fabsf(dP[j][e] * fac[kQInv * kL + t]));
+          big[2] = fmaxf(big[2], fabsf(dW[j][e] * fac[kKInv * kL + q]));
+          big[3] = fmaxf(big[3], fabsf(dW[j][e] * fac[kKInv * kL + t]));
+        }
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        big[m] = warp_max(big[m]);
+        if (lane == 0) most[warp * 4 + m] = big[m];
+      }
+      __syncthreads();  // the columns are read; the matrices take their place
+      Scale sc[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) sc[m] = scale_of(warp_max(lane < 16 ? most[lane * 4 + m] : 0.f));
+      char* mats = smem + (st - su);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int t = ra + r * 8, q = c0 + j * 8 + ca;
+          const float2 ki = *reinterpret_cast<const float2*>(fac + kKInv * kL + q);
+          const float kt = fac[kKInv * kL + t], qt = fac[kQInv * kL + t];
+          const float x = dP[j][2 * r], y = dP[j][2 * r + 1], z = dW[j][2 * r], w = dW[j][2 * r + 1];
+          const float v[4][2] = {{x * ki.x, y * ki.y}, {x * qt, y * qt}, {z * ki.x, w * ki.y}, {z * kt, w * kt}};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            uint32_t hi, lo;
+            split(v[m][0] * sc[m].mul, v[m][1] * sc[m].mul, hi, lo);
+            char* at = mats + m * NP * kTile + piece_at<kL>(t, q) + (q & 7) * 2;
+            *reinterpret_cast<uint32_t*>(at) = hi;
+            if (NP == 2) *reinterpret_cast<uint32_t*>(at + kTile) = lo;
+          }
+        }
+      __syncthreads();
+      const uint32_t ku = su, qu = su + keys_bytes(KP, NP) / 2;
+      constexpr int pk = kL * KP * 2, mat = NP * kTile;
+      zero(acc);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        if (kk <= mt) grad_step<false, false, kL, KP, NP>(acc, st, kTile, r0, ku, pk, k0, kk, 1.f, lane);
+      add_scaled(dq, acc, sc[0].inv);
+      zero(acc);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        if (kk >= mt) grad_step<false, true, kL, KP, NP>(acc, st + mat, kTile, r0, qu, pk, k0, kk, 1.f, lane);
+      add_scaled(dk, acc, sc[1].inv);
+      zero(acc);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        if (kk <= mt) grad_step<false, false, kL, KP, NP>(acc, st + 2 * mat, kTile, r0, ku, pk, k0, kk, 1.f, lane);
+      add_scaled(dk, acc, -sc[2].inv);
+      zero(acc);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        if (kk >= mt) grad_step<false, true, kL, KP, NP>(acc, st + 3 * mat, kTile, r0, ku, pk, k0, kk, 1.f, lane);
+      add_scaled(dk, acc, -sc[3].inv);
+    }
+    if (L::blocks == 1 && i + 1 < total) {
+      __syncthreads();
+      fetch(i + 1);
+    }
   }
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
@@ -486,9 +445,41 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
   }
 }
 
+// dg: what follows a token in its chunk, and the state's share at the chunk's end; dbeta.  One warp a chunk
+// and value head, two tokens a lane; sums over the tiles in order.
+__global__ void __launch_bounds__(128) gdr_gates_kernel(const GdrArgs a, long long records, const Kept kept) {
+  const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, tiles = (a.V + 15) / 16;
+  if (item >= records * a.H) return;
+  const long long rec = item / a.H;
+  const int h = (int)(item % a.H);
+  int n, c;
+  Seq s;
+  if (!find_chunk(a, rec, &n, &s, &c)) return;
+  const size_t base = (size_t)item * tiles;
+  float x[2] = {0.f, 0.f}, b[2] = {0.f, 0.f}, end = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < tiles; ++i) {
+    const float2 d = *reinterpret_cast<const float2*>(kept.dots + (base + i) * kL + 2 * lane);
+    const float2 e = *reinterpret_cast<const float2*>(kept.dbeta + (base + i) * kL + 2 * lane);
+    const float4 f = *reinterpret_cast<const float4*>(kept.ends + (base + i) * kQuarter);
+    x[0] += d.x, x[1] += d.y, b[0] += e.x, b[1] += e.y, end += (f.x + f.y) + (f.z + f.w);
+  }
+  double sum = (double)x[0] + x[1];
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const double y = __shfl_down_sync(0xffffffffu, sum, d);
+    if (lane + d < 32) sum += y;
+  }
+  const int len = (int)min((long long)kL, s.len - (long long)c * kL);
+  const size_t out = ((size_t)s.b * a.H + h) * a.T + s.lo + (long long)c * kL + 2 * lane;
+  if (2 * lane < len) a.dg[out] = (float)(sum + end), a.dbeta[out] = b[0];
+  if (2 * lane + 1 < len) a.dg[out + 1] = (float)(sum - x[0] + end), a.dbeta[out + 1] = b[1];
+}
+
 // The workspace: keys and records, then what Kept lists.
 struct BwdLayout {
-  size_t records, S, S_inv, Z, U, U_inv, dots, D, D_inv, dV, dV_inv, dbeta, ends, total;
+  size_t records, S, S_inv, Z, U, U_inv, dots, D, D_inv, dV, dV_inv, dO, dO_inv, dbeta, ends, total;
 };
 BwdLayout bwd_layout(const GdrArgs& a) {
   const int np = a.dtype ? 1 : 2, KP = a.K <= 64 ? 64 : 128;
@@ -512,6 +503,8 @@ BwdLayout bwd_layout(const GdrArgs& a) {
   l.D_inv = take(rt * 16);
   l.dV = take(rt * np * 2048);
   l.dV_inv = take(rt * 16);
+  l.dO = take(rt * np * 2048);
+  l.dO_inv = take(rt * 16);
   l.dbeta = take(rt * 256);
   l.ends = take(rt * 16);
   l.total = at;
@@ -534,10 +527,11 @@ cudaError_t backward(const GdrArgs& a, char* ws, cudaStream_t stream) {
   const BwdLayout l = bwd_layout(a);
   char* records = ws + l.records;
   Kept k;
-  k.S = (uint4*)(ws + l.S), k.S_inv = (float*)(ws + l.S_inv), k.Z = (float4*)(ws + l.Z);
-  k.U = (uint4*)(ws + l.U), k.U_inv = (float*)(ws + l.U_inv), k.dots = (float*)(ws + l.dots);
-  k.D = (uint4*)(ws + l.D), k.D_inv = (float*)(ws + l.D_inv), k.dV = (uint4*)(ws + l.dV);
-  k.dV_inv = (float*)(ws + l.dV_inv), k.dbeta = (float*)(ws + l.dbeta), k.ends = (float*)(ws + l.ends);
+  k.S = ws + l.S, k.S_inv = (float*)(ws + l.S_inv), k.Z = (float4*)(ws + l.Z);
+  k.U = ws + l.U, k.U_inv = (float*)(ws + l.U_inv), k.dots = (float*)(ws + l.dots);
+  k.D = ws + l.D, k.D_inv = (float*)(ws + l.D_inv), k.dV = ws + l.dV;
+  k.dV_inv = (float*)(ws + l.dV_inv), k.dO = ws + l.dO, k.dO_inv = (float*)(ws + l.dO_inv);
+  k.dbeta = (float*)(ws + l.dbeta), k.ends = (float*)(ws + l.ends);
   cudaError_t e = launch_prep<T, KP, true>(a, ws, records, stream);
   if (e != cudaSuccess) return e;
   e = launch_walk<T, KP, true>(a, ws, records, k, stream);
@@ -551,6 +545,10 @@ cudaError_t backward(const GdrArgs& a, char* ws, cudaStream_t stream) {
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GradStage<T, KP>::bytes);
   if (e != cudaSuccess) return e;
   kernel<<<dim3((unsigned)record_count(a), a.HK), kGradThreads, GradStage<T, KP>::bytes, stream>>>(a, ws, records, k);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const long long items = record_count(a) * a.H;
+  gdr_gates_kernel<<<(unsigned)((items + 3) / 4), 128, 0, stream>>>(a, record_count(a), k);
   return cudaGetLastError();
 }
 

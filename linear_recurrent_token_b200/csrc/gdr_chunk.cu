@@ -14,7 +14,7 @@ constexpr int kMs = kL + 4;  // row pitch of the fp32 matrices: a fragment's lan
 template <int KP, int NP>
 constexpr int prep_smem() {
   constexpr int matrices = (2 * kL + 32) * kMs * 4;  // in the place of k and q
-  return (keys_bytes(KP, NP) > matrices ? keys_bytes(KP, NP) : matrices) + kL * 8 + kFactorBytes + 2 * kL * 4;
+  return (keys_bytes(KP, NP) > matrices ? keys_bytes(KP, NP) : matrices) + kFactorBytes + 2 * kL * 4;
 }
 
 // c += (A diag(b)) B for a 16 x 8 tile of c, k = 8 STEPS: fp32 matrices in shared memory (pitch kMs) as two
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
   float* X = R + kL * kMs;  // [32]
   float* fac = reinterpret_cast<float*>(smem + prep_smem<KP, NP>()) - (kFactors + 2) * kL;
   float* pmax = fac + kFactors * kL;  // [2][64]
-  float2* G = reinterpret_cast<float2*>(fac) - kL;
+  float2* G = reinterpret_cast<float2*>(fac + kG * kL);
   int n, c;
   Seq sq_;
   if (!find_chunk(a, blockIdx.x, &n, &sq_, &c)) return;
@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
       const int t = 2 * lane;
       const double2 sum = cumulative(g, a.sg.t, t0, len, lane);
       const double last = __shfl_sync(0xffffffffu, sum.y, 31);
-      G[t] = two_parts(sum.x), G[t + 1] = two_parts(sum.y);
+      const float2 g0 = two_parts(sum.x), g1 = two_parts(sum.y);
+      G[t] = g0, G[t + 1] = g1;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const double x = e ? sum.y : sum.x;

@@ -46,7 +46,7 @@ constexpr int kQuarter = 4;  // warps of a tile of 16 value columns
 // [64][64] fp16, then the per-token factors.  The 16-byte pieces of a row of these tiles are permuted
 // by the row, so that a record is copied as it is and ldmatrix meets no bank conflicts.
 // kGK = gam / k's scale and so on: what the passes over the chunks multiply by; the rest is for the others.
-enum { kGK = 0, kGQ, kWK, kBeta, kRInv, kPInv, kGam, kW, kKInv, kQInv, kFactors };
+enum { kGK = 0, kGQ, kWK, kBeta, kRInv, kPInv, kGam, kW, kKInv, kQInv, kG, kFactors = kG + 2 };  // kG: G in two parts
 constexpr int kTile = kL * kL * 2;
 constexpr int kFactorBytes = kFactors * kL * 4;
 __host__ __device__ constexpr int keys_bytes(int KP, int np) { return 2 * np * kL * KP * 2; }
@@ -172,6 +172,12 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// c = a b
+__device__ __forceinline__ void mma_new(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // c += a b, tf32 operands
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -260,23 +266,31 @@ __device__ __forceinline__ float tile_max(const float (&c)[N][4]) {
   return warp_max(m);
 }
 
-// One k step of a product of a quarter: acc (two or more tiles of 8 columns) += A B for NA parts of A and
-// NB of B, the planes of B `plane` bytes apart.  lo parts first: they are small, and so is what the
-// tensor cores' sums cut off below them.  load(tile pair, plane) gives the B fragments.
-template <int NT, int NA, int NB, class Load>
+// One k step of a product of a quarter: acc (two or more tiles of 8 columns) += A B, or = A B where FRESH,
+// for NA parts of A and NB of B, the planes of B `plane` bytes apart.  lo parts first: they are small, and
+// so is what the tensor cores' sums cut off below them.  load(tile pair, plane) gives the B fragments.
+template <bool FRESH, int NT, int NA, int NB, class Load>
 __device__ __forceinline__ void step(float (&acc)[NT][4], const uint4& ah, const uint4& al, Load load) {
   const uint32_t hi[4] = {ah.x, ah.y, ah.z, ah.w}, lo[4] = {al.x, al.y, al.z, al.w};
 #pragma unroll
   for (int j = 0; j < NT; j += 2) {
     uint32_t b[4];
     load(b, j, 0);
-    if constexpr (NA == 2) mma(acc[j], lo, b[0], b[1]), mma(acc[j + 1], lo, b[2], b[3]);
+    bool fresh = FRESH;
+    auto add = [&](const uint32_t (&a)[4], const uint32_t (&f)[4]) {
+      if (fresh)
+        mma_new(acc[j], a, f[0], f[1]), mma_new(acc[j + 1], a, f[2], f[3]);
+      else
+        mma(acc[j], a, f[0], f[1]), mma(acc[j + 1], a, f[2], f[3]);
+      fresh = false;
+    };
+    if constexpr (NA == 2) add(lo, b);
     if constexpr (NB == 2) {
       uint32_t l[4];
       load(l, j, 1);
-      mma(acc[j], hi, l[0], l[1]), mma(acc[j + 1], hi, l[2], l[3]);
+      add(hi, l);
     }
-    mma(acc[j], hi, b[0], b[1]), mma(acc[j + 1], hi, b[2], b[3]);
+    add(hi, b);
   }
 }
 template <int NT>

@@ -8,21 +8,24 @@ namespace mlstm {
 namespace gdr {
 
 // What the gradients keep of the two passes, by record of a chunk and value head (states: one more a
-// sequence, the final one) and by tile of 16 value columns.  Operands lie as fragments, 512 bytes a k
-// step; each quarter of the steps has its scale.  NK: parts of an operand that only products rounded
-// to the output's type read, one (11 bits) for bf16, two for fp32.
+// sequence, the final one) and by tile of 16 value columns.  Operands are fp16 tiles [16 values][tokens or
+// keys] with the pieces of a row permuted as in the other records, a tile's parts one behind the other;
+// each quarter of the tokens or keys has its scale.  NK: parts of an operand that only products rounded to
+// the output's type read, one (11 bits) for bf16, two for fp32.
 struct Kept {
-  uint4* S;       // S^T at the chunk's start: [state][tile][2 parts][KP / 16][32]
+  char* S;        // S at the chunk's start: [state][tile][2 parts][16][KP]
   float* S_inv;   // [state][tile][4]
-  float4* Z;      // Z': [record][tile][8][32]
-  uint4* U;       // U^T: [record][tile][NK][4][32]
+  float4* Z;      // Z' as accumulators: [record][tile][8][32]
+  char* U;        // [record][tile][NK][16][64]
   float* U_inv;   // [record][tile][4]
   float* dots;    // dO . O, then dO . O - dV . V, over the tile's columns: [record][tile][64]
   // of the pass backward
-  uint4* D;       // dS^T at the chunk's end: [record][tile][NK][KP / 16][32]
+  char* D;        // dS at the chunk's end: [record][tile][NK][16][KP]
   float* D_inv;   // [record][tile][4]
-  uint4* dV;      // dV^T: [record][tile][NK][4][32]
+  char* dV;       // [record][tile][NK][16][64]
   float* dV_inv;  // [record][tile][4]
+  char* dO;       // [record][tile][NK][16][64]
+  float* dO_inv;  // [record][tile][4]
   float* dbeta;   // dY . Z' over the tile's columns: [record][tile][64]
   float* ends;    // <dS, S> at the chunk's end over the tile's columns and a quarter of the keys: [record][tile][4]
 };
@@ -137,6 +140,37 @@ __device__ __forceinline__ void write_columns(const float (&x)[2][4], char* at, 
   }
 }
 
+// Two accumulator tiles' operand (rows = values, 16 columns from c0) in a kept tile with COLS columns.
+template <int COLS>
+__device__ __forceinline__ void keep16(char* tile, int c0, const uint4& f, int lane) {
+  const int row = lane >> 2, col = c0 + 2 * (lane & 3);
+  char* at = tile + piece_at<COLS>(row, col) + (col & 7) * 2;       // rows r and r + 8 share their permutation
+  char* bt = tile + piece_at<COLS>(row, col + 8) + (col & 7) * 2;
+  *reinterpret_cast<uint32_t*>(at) = f.x;
+  *reinterpret_cast<uint32_t*>(at + 8 * COLS * 2) = f.y;
+  *reinterpret_cast<uint32_t*>(bt) = f.z;
+  *reinterpret_cast<uint32_t*>(bt + 8 * COLS * 2) = f.w;
+}
+template <int COLS>
+__device__ __forceinline__ uint4 kept16(const char* tile, int c0, int lane) {
+  const int row = lane >> 2, col = c0 + 2 * (lane & 3);
+  const char* at = tile + piece_at<COLS>(row, col) + (col & 7) * 2;
+  const char* bt = tile + piece_at<COLS>(row, col + 8) + (col & 7) * 2;
+  return make_uint4(*reinterpret_cast<const uint32_t*>(at), *reinterpret_cast<const uint32_t*>(at + 8 * COLS * 2),
+                    *reinterpret_cast<const uint32_t*>(bt), *reinterpret_cast<const uint32_t*>(bt + 8 * COLS * 2));
+}
+// The quarter w of a token operand: its parts and its scale.
+template <int NK>
+__device__ __forceinline__ void keep_tokens(char* tiles, float* inv, size_t tile, const float (&x)[2][4], const Scale& sc, int w,
+                                            int lane) {
+  uint4 hi, lo;
+  split_a(x[0], x[1], sc.mul, hi, lo);
+  char* at = tiles + tile * NK * 16 * kL * 2;
+  keep16<kL>(at, w * 16, hi, lane);
+  if (NK == 2) keep16<kL>(at + 16 * kL * 2, w * 16, lo, lane);
+  if (lane == 0) inv[tile * kQuarter + w] = sc.inv;
+}
+
 // A quarter of an operand into exchange: its k steps (STEPS of them) in two parts, or one, with its scale.
 template <int STEPS, int PARTS>
 __device__ __forceinline__ void give(const float (&x)[2 * STEPS][4], const Scale& sc, char* to, float* inv, int w, int lane) {
@@ -163,19 +197,25 @@ template <int KP, int NP, bool TWO, bool LO2>
 __device__ __forceinline__ void by_keys(float (&x)[2][4], float (&y)[2][4], const char* f, const float* inv, uint32_t k,
                                         uint32_t q, int w, int lane) {
   constexpr int KS = KP / 16 / kQuarter;
-  zero(x), zero(y);
+  zero(x);
+  if constexpr (TWO) zero(y);
 #pragma unroll
   for (int b = 0; b < kQuarter; ++b) {
     float tx[2][4], ty[2][4];
-    zero(tx), zero(ty);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       uint4 hi, lo;
       take<2>(f, b * KS + i, lane, hi, lo);
       const int at = piece_at<KP>(w * 16 + b_row(lane), (b * KS + i) * 16 + b_col(lane));
-      step<2, 2, NP>(tx, hi, lo, [&](uint32_t (&r)[4], int, int plane) { ldsm4(r, k + at + plane * kL * KP * 2); });
-      if constexpr (TWO)
-        step<2, LO2 ? 2 : 1, NP>(ty, hi, lo, [&](uint32_t (&r)[4], int, int plane) { ldsm4(r, q + at + plane * kL * KP * 2); });
+      auto from_k = [&](uint32_t (&r)[4], int, int plane) { ldsm4(r, k + at + plane * kL * KP * 2); };
+      auto from_q = [&](uint32_t (&r)[4], int, int plane) { ldsm4(r, q + at + plane * kL * KP * 2); };
+      if (i == 0) {
+        step<true, 2, 2, NP>(tx, hi, lo, from_k);
+        if constexpr (TWO) step<true, 2, LO2 ? 2 : 1, NP>(ty, hi, lo, from_q);
+      } else {
+        step<false, 2, 2, NP>(tx, hi, lo, from_k);
+        if constexpr (TWO) step<false, 2, LO2 ? 2 : 1, NP>(ty, hi, lo, from_q);
+      }
     }
     add_scaled(x, tx, inv[b]);
     if constexpr (TWO) add_scaled(y, ty, inv[b]);
@@ -191,12 +231,11 @@ __device__ __forceinline__ void by_tokens(float (&x)[2][4], const char* f, const
   for (int b = 0; b < kQuarter; ++b) {
     if (TRANS ? b < w : b > w) continue;
     float t[2][4];
-    zero(t);
     uint4 hi, lo;
     take<NA>(f, b, lane, hi, lo);
     const int at = TRANS ? piece_at<kL>(b * 16 + bt_row(lane), w * 16 + bt_col(lane))
                          : piece_at<kL>(w * 16 + b_row(lane), b * 16 + b_col(lane));
-    step<2, NA, NX>(t, hi, lo, [&](uint32_t (&r)[4], int, int plane) {
+    step<true, 2, NA, NX>(t, hi, lo, [&](uint32_t (&r)[4], int, int plane) {
       if constexpr (TRANS)
         ldsm4t(r, tile + at + plane * kTile);
       else
@@ -217,10 +256,9 @@ __device__ __forceinline__ void to_state(float (&S)[KP / 32][4], float keep, con
 #pragma unroll
   for (int b = 0; b < kQuarter; ++b) {
     float d[KP / 32][4];
-    zero(d);
     uint4 hi, lo;
     take<2>(f, b, lane, hi, lo);
-    step<KP / 32, 2, NP>(d, hi, lo, [&](uint32_t (&r)[4], int j, int plane) {
+    step<true, KP / 32, 2, NP>(d, hi, lo, [&](uint32_t (&r)[4], int j, int plane) {
       ldsm4t(r, tile + piece_at<KP>(b * 16 + bt_row(lane), w * (KP / 4) + j * 8 + bt_col(lane)) + plane * kL * KP * 2);
     });
     add_scaled(S, d, inv[b]);
@@ -264,8 +302,9 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_walk_kernel(const GdrA
       for (int i = 0; i < KS; ++i) {
         uint4 hi, lo;
         split_a(S[2 * i], S[2 * i + 1], sc.mul, hi, lo);
-        kept.S[(base * 2 * (KP / 16) + w * KS + i) * 32 + lane] = hi;
-        kept.S[((base * 2 + 1) * (KP / 16) + w * KS + i) * 32 + lane] = lo;
+        char* at = kept.S + base * 2 * 16 * KP * 2;
+        keep16<KP>(at, (w * KS + i) * 16, hi, lane);
+        keep16<KP>(at + 16 * KP * 2, (w * KS + i) * 16, lo, lane);
       }
     }
   };
@@ -333,11 +372,7 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_walk_kernel(const GdrA
         if (live) {
           kept.Z[(base * 8 + 2 * w) * 32 + lane] = make_float4(z[0][0], z[0][1], z[0][2], z[0][3]);
           kept.Z[(base * 8 + 2 * w + 1) * 32 + lane] = make_float4(z[1][0], z[1][1], z[1][2], z[1][3]);
-          uint4 hi, lo;
-          split_a(u[0], u[1], sc.mul, hi, lo);
-          if (lane == 0) kept.U_inv[base * kQuarter + w] = sc.inv;
-          kept.U[(base * NK * 4 + w) * 32 + lane] = hi;
-          if (NK == 2) kept.U[((base * NK + 1) * 4 + w) * 32 + lane] = lo;
+          keep_tokens<NK>(kept.U, kept.U_inv, base, u, sc, w, lane);
         }
       }
     }
