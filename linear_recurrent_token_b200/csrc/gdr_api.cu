@@ -87,6 +87,7 @@ GdrArgs gdr_args(const mlstm_gdr_params_t* p, const GdrShape& s) {
   a.N = (int)s.N, a.HK = p->HK, a.H = p->H, a.T = p->T, a.K = p->K, a.V = p->V;
   a.dtype = p->dtype == MLSTM_BF16 ? 1 : 0;
   a.packed = p->num_seqs > 0 ? 1 : 0;
+  a.wait = p->wait_limit_cycles > 0 ? p->wait_limit_cycles : 0;
   a.sq = to_stride(p->q), a.sk = to_stride(p->k), a.sv = to_stride(p->v);
   a.sg = to_stride(p->g), a.sb = to_stride(p->beta), a.so = to_stride(p->o);
   return a;
@@ -245,6 +246,19 @@ mlstm_status_t mlstm_gdr_bwd(const mlstm_gdr_params_t* p, const void* q, const v
   a.sdq = to_stride(s_dq), a.sdk = to_stride(s_dk), a.sdv = to_stride(s_dv);
   a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dS0 = dS0;
   return done(launch_gdr_bwd(a, workspace, (cudaStream_t)stream));
+}
+
+mlstm_status_t mlstm_gdr_status(const mlstm_gdr_params_t* p, int backward, const void* workspace, mlstm_stream_t stream) {
+  GdrShape s;
+  mlstm_status_t st = check_gdr(p, backward != 0, &s);
+  if (st != MLSTM_OK) return st;
+  const bool waits = s.chunk && s.any && gdr_tc_pass(gdr_args(p, s));
+  if (waits && !workspace) return MLSTM_ERR_NULL;
+  if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return MLSTM_ERR_CUDA;
+  if (!waits) return MLSTM_OK;
+  unsigned int word = 0;
+  if (cudaMemcpy(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return MLSTM_ERR_CUDA;
+  return word == 0 ? MLSTM_OK : MLSTM_ERR_TIMEOUT;
 }
 
 static mlstm_status_t check_rms(const mlstm_rms_params_t* p, bool backward, int* group) {

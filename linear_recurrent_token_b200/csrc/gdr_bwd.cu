@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
   constexpr int fy = L::fs;
   extern __shared__ __align__(128) char smem[];
   const int n = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int local = warp / kQuarter, w = warp % kQuarter, tile = blockIdx.x * TN + local, tiles = (a.V + 15) / 16;
+  const int local = warp / kQuarter, w = (warp + local) % kQuarter, tile = blockIdx.x * TN + local, tiles = (a.V + 15) / 16;
   const int col0 = blockIdx.x * 16 * TN, v0 = tile * 16, cols = min(16, a.V - v0);
   const bool live = tile < tiles;
   const Seq s = sequence(a, n);
@@ -112,8 +112,13 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
     }
     // dU = w (K dS) + P^T dO
     by_keys<KP, NP, false, false>(x, y, ex + L::fs, inv, smem_u32(st), 0u, w, lane);
-    float4 z0 = make_float4(0.f, 0.f, 0.f, 0.f), z1 = z0;
-    if (live) z0 = kept.Z[(base * 8 + 2 * w) * 32 + lane], z1 = kept.Z[(base * 8 + 2 * w + 1) * 32 + lane];
+    float2 zp[2][2];  // Z' of this quarter: [tile of 8 tokens][row r or r + 8]
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        zp[j][r] = live ? *reinterpret_cast<const float2*>(kept.Z + (base * 16 + ra + 8 * r) * kL + w * 16 + 8 * j + ca)
+                        : make_float2(0.f, 0.f);
     cp_wait<L::chunks == 2 ? 1 : 0>();
     __syncthreads();  // R and P have come, dO is in exchange, dS has been read
     by_tokens<true, NP, 2>(y, ex + L::fu, inv + 2 * kQuarter, smem_u32(mats) + 2 * kTile, w, lane);
@@ -137,11 +142,10 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float2 be = factor(fac + kBeta * kL, w * 16, j, lane), gk = factor(fac + kGK * kL, w * 16, j, lane);
-        const float4 z = j ? z1 : z0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[j][e] += y[j][e];
-        dot[2 * j] = x[j][0] * z.x + x[j][2] * z.z;
-        dot[2 * j + 1] = x[j][1] * z.y + x[j][3] * z.w;
+        dot[2 * j] = x[j][0] * zp[j][0].x + x[j][2] * zp[j][1].x;
+        dot[2 * j + 1] = x[j][1] * zp[j][0].y + x[j][3] * zp[j][1].y;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x[j][e] *= e & 1 ? be.y : be.x;
@@ -284,11 +288,11 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
     const int live = min(4, tiles - first);
     // PARTS: parts in memory, of which NP are read
     auto operand = [&](const char* from, size_t at, int PARTS, int at_smem, int cols) {
-      const int per = 16 * cols * 2 / 16;  // pieces of a tile's part
+      const int per = 16 * cols * 2 / 16;  // pieces of a tile's part, 128 to a block of 64 columns
       for (int e = tid; e < 4 * NP * per; e += kGradThreads) {
         const int x = e % per, part = e / per % NP, tile = e / (per * NP);
         const bool in = tile < live;
-        cp_async16(to + at_smem + part * kVB * cols * 2 + (tile * per + x) * 16,
+        cp_async16(to + at_smem + part * kVB * cols * 2 + (x / 128 * kVB + tile * 16) * 128 + x % 128 * 16,
                    from + ((at + (in ? tile : 0)) * PARTS + part) * 16 * cols * 2 + x * 16, in);
       }
     };
@@ -486,7 +490,7 @@ BwdLayout bwd_layout(const GdrArgs& a) {
   const size_t nrec = (size_t)record_count(a), tiles = (a.V + 15) / 16;
   const size_t rt = nrec * a.H * tiles, st = (nrec + a.N) * a.H * tiles, key_step = (size_t)(KP / 16) * 512;
   BwdLayout l;
-  size_t at = nrec * a.HK * keys_bytes(KP, np);
+  size_t at = kGdrHeader + nrec * a.HK * keys_bytes(KP, np);
   auto take = [&](size_t n) {
     const size_t here = at;
     at += (n + 255) & ~(size_t)255;
@@ -525,26 +529,29 @@ cudaError_t launch_back(const GdrArgs& a, const char* keys, const char* records,
 template <typename T, int KP>
 cudaError_t backward(const GdrArgs& a, char* ws, cudaStream_t stream) {
   const BwdLayout l = bwd_layout(a);
-  char* records = ws + l.records;
+  char *keys = ws + kGdrHeader, *records = ws + l.records;
   Kept k;
-  k.S = ws + l.S, k.S_inv = (float*)(ws + l.S_inv), k.Z = (float4*)(ws + l.Z);
+  k.S = ws + l.S, k.S_inv = (float*)(ws + l.S_inv), k.Z = (float*)(ws + l.Z);
   k.U = ws + l.U, k.U_inv = (float*)(ws + l.U_inv), k.dots = (float*)(ws + l.dots);
   k.D = ws + l.D, k.D_inv = (float*)(ws + l.D_inv), k.dV = ws + l.dV;
   k.dV_inv = (float*)(ws + l.dV_inv), k.dO = ws + l.dO, k.dO_inv = (float*)(ws + l.dO_inv);
   k.dbeta = (float*)(ws + l.dbeta), k.ends = (float*)(ws + l.ends);
-  cudaError_t e = launch_prep<T, KP, true>(a, ws, records, stream);
+  cudaError_t e = launch_prep<T, KP, true>(a, keys, records, stream);
   if (e != cudaSuccess) return e;
-  e = launch_walk<T, KP, true>(a, ws, records, k, stream);
+  bool walked = false;
+  if constexpr (sizeof(T) == 2)
+    if ((walked = gdr_tc_pass(a))) e = launch_tc_walk<KP, true>(a, keys, records, k, (unsigned int*)ws, stream);
+  if (!walked) e = launch_walk<T, KP, true>(a, keys, records, k, stream);
   if (e != cudaSuccess) return e;
   const int tn = tiles_a_block<T>(a);
   if constexpr (sizeof(T) == 2)
-    if (tn == 4) e = launch_back<T, KP, 4>(a, ws, records, k, stream);
-  if (tn != 4) e = tn == 2 ? launch_back<T, KP, 2>(a, ws, records, k, stream) : launch_back<T, KP, 1>(a, ws, records, k, stream);
+    if (tn == 4) e = launch_back<T, KP, 4>(a, keys, records, k, stream);
+  if (tn != 4) e = tn == 2 ? launch_back<T, KP, 2>(a, keys, records, k, stream) : launch_back<T, KP, 1>(a, keys, records, k, stream);
   if (e != cudaSuccess) return e;
   const auto kernel = gdr_grad_kernel<T, KP>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GradStage<T, KP>::bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3((unsigned)record_count(a), a.HK), kGradThreads, GradStage<T, KP>::bytes, stream>>>(a, ws, records, k);
+  kernel<<<dim3((unsigned)record_count(a), a.HK), kGradThreads, GradStage<T, KP>::bytes, stream>>>(a, keys, records, k);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const long long items = record_count(a) * a.H;

@@ -308,12 +308,15 @@ template cudaError_t launch_prep<__nv_bfloat16, 128, true>(const GdrArgs&, char*
 namespace {
 
 template <typename T, int KP>
-cudaError_t chunk(const GdrArgs& a, void* ws, cudaStream_t stream) {
+cudaError_t chunk(const GdrArgs& a, char* ws, cudaStream_t stream) {
   constexpr bool P2 = sizeof(T) == 4;
-  char* keys = (char*)ws;
+  char* keys = ws + kGdrHeader;
   char* records = keys + record_count(a) * a.HK * keys_bytes(KP, sizeof(T) == 4 ? 2 : 1);
   cudaError_t e = launch_prep<T, KP, P2>(a, keys, records, stream);
-  return e != cudaSuccess ? e : launch_walk<T, KP, false>(a, keys, records, Kept{}, stream);
+  if (e != cudaSuccess) return e;
+  if constexpr (sizeof(T) == 2)
+    if (gdr_tc_pass(a)) return launch_tc_walk<KP, false>(a, keys, records, Kept{}, (unsigned int*)ws, stream);
+  return launch_walk<T, KP, false>(a, keys, records, Kept{}, stream);
 }
 
 }  // namespace
@@ -321,13 +324,16 @@ cudaError_t chunk(const GdrArgs& a, void* ws, cudaStream_t stream) {
 
 bool gdr_chunk_supported(int K) { return K <= 128; }
 
+bool gdr_tc_pass(const GdrArgs& a) { return a.dtype == 1 && a.V > 32 && (long long)a.N * a.H * ((a.V + 127) / 128) >= 32; }
+
 size_t gdr_chunk_workspace_bytes(const GdrArgs& a) {
   const int np = a.dtype ? 1 : 2, KP = a.K <= 64 ? 64 : 128;
-  return (size_t)gdr::record_count(a) *
-         ((size_t)a.HK * gdr::keys_bytes(KP, np) + (size_t)a.H * gdr::record_bytes(a.dtype == 0));
+  return kGdrHeader + (size_t)gdr::record_count(a) *
+                          ((size_t)a.HK * gdr::keys_bytes(KP, np) + (size_t)a.H * gdr::record_bytes(a.dtype == 0));
 }
 
-cudaError_t launch_gdr_chunk(const GdrArgs& a, void* ws, cudaStream_t stream) {
+cudaError_t launch_gdr_chunk(const GdrArgs& a, void* workspace, cudaStream_t stream) {
+  char* ws = (char*)workspace;
   if (a.dtype)
     return a.K <= 64 ? gdr::chunk<__nv_bfloat16, 64>(a, ws, stream) : gdr::chunk<__nv_bfloat16, 128>(a, ws, stream);
   return a.K <= 64 ? gdr::chunk<float, 64>(a, ws, stream) : gdr::chunk<float, 128>(a, ws, stream);

@@ -51,10 +51,11 @@ constexpr int kTile = kL * kL * 2;
 constexpr int kFactorBytes = kFactors * kL * 4;
 __host__ __device__ constexpr int keys_bytes(int KP, int np) { return 2 * np * kL * KP * 2; }
 __host__ __device__ constexpr int record_bytes(bool p2) { return (p2 ? 4 : 3) * kTile + kFactorBytes; }
-// byte offset of the 16-byte piece that holds (row, col) of a tile with W columns
-template <int W>
+// Byte offset of the 16-byte piece that holds (row, col) of a tile with W columns: blocks of 64 columns (128
+// bytes a row, ROWS rows), as the tensor cores' 128-byte swizzle has it.
+template <int W, int ROWS = kL>
 __device__ __forceinline__ int piece_at(int row, int col) {
-  return row * W * 2 + (((col >> 3) ^ (row & 7)) << 4);
+  return (W > 64 ? (col >> 6) * (ROWS * 128) : 0) + row * 128 + ((((col >> 3) ^ row) & 7) << 4);
 }
 
 // ------------------------------------------------------------------------------------- sequences

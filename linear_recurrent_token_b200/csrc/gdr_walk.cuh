@@ -15,7 +15,7 @@ namespace gdr {
 struct Kept {
   char* S;        // S at the chunk's start: [state][tile][2 parts][16][KP]
   float* S_inv;   // [state][tile][4]
-  float4* Z;      // Z' as accumulators: [record][tile][8][32]
+  float* Z;       // Z': [record][tile][16][64]
   char* U;        // [record][tile][NK][16][64]
   float* U_inv;   // [record][tile][4]
   float* dots;    // dO . O, then dO . O - dV . V, over the tile's columns: [record][tile][64]
@@ -32,6 +32,9 @@ struct Kept {
 template <typename T>
 constexpr int kept_parts() { return sizeof(T) == 4 ? 2 : 1; }
 
+template <int KP, bool GRAD>
+cudaError_t launch_tc_walk(const GdrArgs& a, const char* keys, const char* records, const Kept& kept, unsigned int* err,
+                           cudaStream_t stream);
 template <typename T, int KP, bool P2>
 cudaError_t launch_prep(const GdrArgs& a, char* keys, char* records, cudaStream_t stream);
 
@@ -144,20 +147,20 @@ __device__ __forceinline__ void write_columns(const float (&x)[2][4], char* at, 
 template <int COLS>
 __device__ __forceinline__ void keep16(char* tile, int c0, const uint4& f, int lane) {
   const int row = lane >> 2, col = c0 + 2 * (lane & 3);
-  char* at = tile + piece_at<COLS>(row, col) + (col & 7) * 2;       // rows r and r + 8 share their permutation
-  char* bt = tile + piece_at<COLS>(row, col + 8) + (col & 7) * 2;
+  char* at = tile + piece_at<COLS, 16>(row, col) + (col & 7) * 2;  // rows r and r + 8 share their permutation
+  char* bt = tile + piece_at<COLS, 16>(row, col + 8) + (col & 7) * 2;
   *reinterpret_cast<uint32_t*>(at) = f.x;
-  *reinterpret_cast<uint32_t*>(at + 8 * COLS * 2) = f.y;
+  *reinterpret_cast<uint32_t*>(at + 8 * 128) = f.y;
   *reinterpret_cast<uint32_t*>(bt) = f.z;
-  *reinterpret_cast<uint32_t*>(bt + 8 * COLS * 2) = f.w;
+  *reinterpret_cast<uint32_t*>(bt + 8 * 128) = f.w;
 }
 template <int COLS>
 __device__ __forceinline__ uint4 kept16(const char* tile, int c0, int lane) {
   const int row = lane >> 2, col = c0 + 2 * (lane & 3);
-  const char* at = tile + piece_at<COLS>(row, col) + (col & 7) * 2;
-  const char* bt = tile + piece_at<COLS>(row, col + 8) + (col & 7) * 2;
-  return make_uint4(*reinterpret_cast<const uint32_t*>(at), *reinterpret_cast<const uint32_t*>(at + 8 * COLS * 2),
-                    *reinterpret_cast<const uint32_t*>(bt), *reinterpret_cast<const uint32_t*>(bt + 8 * COLS * 2));
+  const char* at = tile + piece_at<COLS, 16>(row, col) + (col & 7) * 2;
+  const char* bt = tile + piece_at<COLS, 16>(row, col + 8) + (col & 7) * 2;
+  return make_uint4(*reinterpret_cast<const uint32_t*>(at), *reinterpret_cast<const uint32_t*>(at + 8 * 128),
+                    *reinterpret_cast<const uint32_t*>(bt), *reinterpret_cast<const uint32_t*>(bt + 8 * 128));
 }
 // The quarter w of a token operand: its parts and its scale.
 template <int NK>
@@ -274,7 +277,8 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_walk_kernel(const GdrA
   constexpr bool FINE = L::P2;  // the output in fp32 accuracy: two parts of S, U and P under it
   extern __shared__ __align__(128) char smem[];
   const int n = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int local = warp / kQuarter, w = warp % kQuarter, tile = blockIdx.x * TN + local, tiles = (a.V + 15) / 16;
+  // the quarters' shares of the triangular products differ: over the tiles, each scheduler gets all of them
+  const int local = warp / kQuarter, w = (warp + local) % kQuarter, tile = blockIdx.x * TN + local, tiles = (a.V + 15) / 16;
   const int col0 = blockIdx.x * 16 * TN, v0 = tile * 16, cols = min(16, a.V - v0);  // cols <= 0 behind the last
   const bool live = tile < tiles;
   const Seq s = sequence(a, n);
@@ -370,8 +374,12 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_walk_kernel(const GdrA
       give<1, L::nu>(u, sc, ex + L::fu, inv + 2 * kQuarter, w, lane);
       if constexpr (GRAD) {
         if (live) {
-          kept.Z[(base * 8 + 2 * w) * 32 + lane] = make_float4(z[0][0], z[0][1], z[0][2], z[0][3]);
-          kept.Z[(base * 8 + 2 * w + 1) * 32 + lane] = make_float4(z[1][0], z[1][1], z[1][2], z[1][3]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              *reinterpret_cast<float2*>(kept.Z + (base * 16 + ra + 8 * r) * kL + w * 16 + 8 * j + ca) =
+                  make_float2(z[j][2 * r], z[j][2 * r + 1]);
           keep_tokens<NK>(kept.U, kept.U_inv, base, u, sc, w, lane);
         }
       }

@@ -151,6 +151,7 @@ struct GdrStride {
 };
 struct GdrArgs {
   int N, HK, H, T, K, V, dtype, packed;
+  long long wait;      // bound of the tcgen05 kernels' waits (SM cycles), 0 = default
   const int* offsets;  // [N + 1] where packed
   const void *q, *k, *v;
   const float *g, *beta, *S0;
@@ -167,6 +168,10 @@ struct GdrArgs {
 cudaError_t launch_gdr_recurrent(const GdrArgs& a, cudaStream_t stream);
 // chunks of 64 tokens on the tensor cores (gdr_chunk.cu)
 constexpr int kGdrChunkFrom = 32;
+// Head of the chunk kernels' workspace: its first word is the error word of the tcgen05 pass (1: a wait ran
+// out).  gdr_tc_pass: whether a call runs that pass (known from its sizes).
+constexpr size_t kGdrHeader = 256;
+bool gdr_tc_pass(const GdrArgs& a);
 bool gdr_chunk_supported(int K);
 size_t gdr_chunk_workspace_bytes(const GdrArgs& a);
 cudaError_t launch_gdr_chunk(const GdrArgs& a, void* ws, cudaStream_t stream);

@@ -52,7 +52,7 @@ class GdrParams(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("HK", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int),
                 ("K", ctypes.c_int), ("V", ctypes.c_int), ("num_seqs", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("mode", ctypes.c_int), ("q", GdrStride), ("k", GdrStride), ("v", GdrStride), ("g", GdrStride),
-                ("beta", GdrStride), ("o", GdrStride)]
+                ("beta", GdrStride), ("o", GdrStride), ("wait_limit_cycles", ctypes.c_longlong)]
 
 
 class GdrStepParams(ctypes.Structure):
@@ -179,6 +179,8 @@ def _load(path):
     L.mlstm_gdr_bwd_workspace_size.restype = Z
     L.mlstm_gdr_bwd.argtypes = [P] + [P] * 9 + [GdrStride] * 3 + [P] * 7 + [Z, P]
     L.mlstm_gdr_bwd.restype = I
+    L.mlstm_gdr_status.argtypes = [P, I, P, P]
+    L.mlstm_gdr_status.restype = I
     L.mlstm_rms_norm.argtypes = [P] + [P] * 7
     L.mlstm_rms_norm.restype = I
     L.mlstm_rms_norm_bwd_workspace_size.argtypes = [P]
@@ -549,7 +551,7 @@ def step(q, k, v, igate, fgate, C, n, m, ogate=None, *, num_blocks: int = 1, ret
 # structs are packed in one go, and the device and the stream are switched only where they have to be.
 
 _F32 = torch.float32
-_GDR_PACK = struct.Struct("9i18q")      # GdrParams
+_GDR_PACK = struct.Struct("9i19q")      # GdrParams
 _GDR_STEP_PACK = struct.Struct("7i18q")  # GdrStepParams
 _RMS_PACK = struct.Struct("q4if4x")     # RmsParams
 
@@ -637,9 +639,9 @@ def _gdr_inputs(q, k, v, g, beta):
         + _strides("beta", beta, False)
 
 
-def _gdr_pack(sizes, num_seqs, dtype, mode, inputs, so):
+def _gdr_pack(sizes, num_seqs, dtype, mode, inputs, so, wait_limit_cycles):
     B, HK, H, T, K, V, _ = sizes
-    return _GDR_PACK.pack(B, HK, H, T, K, V, num_seqs, _DTYPES[dtype], mode, *inputs, *so)
+    return _GDR_PACK.pack(B, HK, H, T, K, V, num_seqs, _DTYPES[dtype], mode, *inputs, *so, wait_limit_cycles)
 
 
 def _gdr_mode(mode):
@@ -648,13 +650,14 @@ def _gdr_mode(mode):
     return GDR_MODES[mode]
 
 
-def gdr_params(q, k, v, g, beta, o=None, seq_offsets=None, mode: str = "auto") -> GdrParams:
+def gdr_params(q, k, v, g, beta, o=None, seq_offsets=None, mode: str = "auto",
+               wait_limit_cycles: int = 0) -> GdrParams:
     """Sizes and strides of a call; o: the output, or the gradient of it (None: dense like v's shape)."""
     sizes = _gdr_shapes(q, k, v, g, beta, seq_offsets)
     B, HK, H, T, K, V, N = sizes
     so = (H * T * V, T * V, V) if o is None else _strides("o", o)
     return GdrParams.from_buffer_copy(_gdr_pack(sizes, 0 if seq_offsets is None else N, q.dtype, _gdr_mode(mode),
-                                                _gdr_inputs(q, k, v, g, beta), so))
+                                                _gdr_inputs(q, k, v, g, beta), so, wait_limit_cycles))
 
 
 def gdr_fwd_workspace_size(params: GdrParams) -> int:
@@ -665,6 +668,12 @@ def gdr_bwd_workspace_size(params: GdrParams) -> int:
     return int(lib().mlstm_gdr_bwd_workspace_size(ctypes.byref(params)))
 
 
+def gdr_status(params: GdrParams, workspace, *, backward: bool = False, stream=None) -> int:
+    """Outcome of the bounded waits of the last gdr_fwd (or gdr_bwd) with these params and this workspace
+    (mlstm_gdr_status; synchronises): 0 ok, 8 a wait ran out (MLSTM_ERR_TIMEOUT)."""
+    return int(lib().mlstm_gdr_status(ctypes.byref(params), int(backward), _ptr(workspace), _stream_ptr(stream)))
+
+
 def _like(t, packed):
     """An output laid out like t where t fills its memory, else dense; zeros where packed sequences may
     leave tokens out."""
@@ -672,7 +681,7 @@ def _like(t, packed):
 
 
 def gdr_fwd(q, k, v, g, beta, S0=None, *, seq_offsets=None, mode: str = "auto", o=None, S_out=None,
-            return_state: bool = True, workspace=None, stream=None):
+            return_state: bool = True, workspace=None, stream=None, wait_limit_cycles: int = 0):
     """The gated delta rule over sequences (mlstm_gdr_fwd): q, k [B,HK,T,K], v [B,H,T,V] (fp32 or bf16,
     H a multiple of HK); g (log decay), beta [B,H,T] fp32; S0 [N,H,K,V] fp32 or None.  Tensors may be
     strided views with a contiguous last axis (a projection's [B,T,heads,width], transposed).
@@ -691,7 +700,8 @@ def gdr_fwd(q, k, v, g, beta, S0=None, *, seq_offsets=None, mode: str = "auto", 
     def body(cs):
         out = _like(v, seq_offsets is not None) if o is None else o
         last = torch.empty(states, dtype=_F32, device=dev) if return_state and S_out is None else S_out
-        p = _gdr_pack(sizes, 0 if seq_offsets is None else N, q.dtype, code, inputs, so or _strides("o", out))
+        p = _gdr_pack(sizes, 0 if seq_offsets is None else N, q.dtype, code, inputs,
+                      so or _strides("o", out), wait_limit_cycles)
         L = lib()
         ws, ws_len = _workspace(workspace, L.mlstm_gdr_fwd_workspace_size(p), dev)
         st = L.mlstm_gdr_fwd(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0),
@@ -735,7 +745,8 @@ def gdr_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None):
     return _on(dev, stream, (q, k, v, g, beta, S, slots, o), body)
 
 
-def gdr_bwd(q, k, v, g, beta, do, S0=None, dS=None, *, seq_offsets=None, workspace=None, stream=None):
+def gdr_bwd(q, k, v, g, beta, do, S0=None, dS=None, *, seq_offsets=None, workspace=None, stream=None,
+            wait_limit_cycles: int = 0):
     """Gradients of the gated delta rule (mlstm_gdr_bwd): gdr_fwd's inputs, do [B,H,T,V] and dS
     [N,H,K,V] fp32 (the gradient of the final states) or None.  Returns a dict: dq, dk, dv in the inputs'
     type, laid out like them where they fill their memory; dg, dbeta [B,H,T] and dS0 [N,H,K,V] fp32.
@@ -747,7 +758,8 @@ def gdr_bwd(q, k, v, g, beta, do, S0=None, dS=None, *, seq_offsets=None, workspa
     _want("S0", S0, states, _F32, dev)
     _want("dS", dS, states, _F32, dev)
     packed = seq_offsets is not None
-    p = _gdr_pack(sizes, N if packed else 0, q.dtype, 0, _gdr_inputs(q, k, v, g, beta), _strides("do", do))
+    p = _gdr_pack(sizes, N if packed else 0, q.dtype, 0, _gdr_inputs(q, k, v, g, beta), _strides("do", do),
+                  wait_limit_cycles)
 
     def body(cs):
         new = torch.zeros if packed else torch.empty

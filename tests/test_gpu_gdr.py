@@ -221,6 +221,86 @@ def test_values_that_are_not_finite_stay_in_their_head(mode):
     assert bool(torch.isfinite(o2[1, 0, :64].float()).all())
 
 
+MANY = [  # enough heads for the tcgen05 pass: B, HK, H, T, K, V
+    (8, 4, 4, 130, 128, 128), (4, 4, 8, 64, 64, 64), (2, 8, 16, 200, 96, 88), (3, 4, 12, 65, 40, 40), (4, 4, 8, 63, 128, 256),
+    (2, 16, 32, 33, 16, 136), (33, 1, 1, 129, 128, 48),
+]
+
+
+@pytest.mark.parametrize("shape", MANY)
+def test_many_heads(shape):
+    inp = inputs.gdr_inputs(*shape, "bf16", seed=sum(shape))
+    B, HK, H, T, K, V = shape
+    t = to_dev(inp, "bf16")
+    a = [t[n] for n in ("q", "k", "v", "g", "beta", "S0")]
+    o, S = Guarded((B, H, T, V), torch.bfloat16), Guarded((B, H, K, V), torch.float32)
+    p = mlstm.gdr_params(*a[:5], o.t)
+    ws = torch.empty(mlstm.gdr_fwd_workspace_size(p), dtype=torch.uint8, device="cuda")
+    mlstm.gdr_fwd(*a, o=o.t, S_out=S.t, workspace=ws)
+    assert mlstm.gdr_status(p, ws) == 0
+    o_ref, S_ref = oracle.gdr_sequential(*(inp[n] for n in ("q", "k", "v", "g", "beta", "S0")))
+    close(o.t, o_ref, "bf16", coarse(inp, "bf16", "chunk"))
+    close(S.t, S_ref, "f32")
+    assert o.intact() and S.intact()
+    o2, S2 = mlstm.gdr_fwd(*a)
+    assert torch.equal(o.t, o2) and torch.equal(S.t, S2)
+
+
+def test_many_heads_packed_strided_and_extreme():
+    """Unlike lengths, token-major views, full resets and values that are not finite, on the tcgen05 pass."""
+    lengths, T, H = (70, 0, 1, 64, 130, 5), 273, 8
+    inp = inputs.gdr_inputs(1, 4, H, T, 64, 48, "bf16", seed=6)
+    rng = np.random.default_rng(6)
+    inp["S0"] = (0.1 * rng.standard_normal((6, H, 64, 48))).astype(np.float32)
+    inp["g"][0, 0, ::7] = -np.inf
+    inp["g"][0, 1] *= 300
+    inp["beta"][0, 2] = 0.0
+    o_ref, S_ref, off, terms = packed(inp, lengths)
+    t = to_dev(inp, "bf16")
+    flip = lambda x: x.transpose(1, 2).contiguous().transpose(1, 2)
+    a = [flip(t[n]) for n in ("q", "k", "v", "g", "beta")]
+    o = torch.full((1, T, H, 48), 7.0, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    _, S = mlstm.gdr_fwd(*a, t["S0"], seq_offsets=off, mode="chunk", o=o)
+    used = sum(lengths)
+    close(o[:, :, :used], o_ref[:, :, :used], "bf16", terms[:, :, :used])
+    close(S, S_ref, "f32")
+    assert bool((o[:, :, used:] == 7.0).all())
+    a[2][0, 3, 75] = float("nan")
+    o2, S2 = mlstm.gdr_fwd(*a, t["S0"], seq_offsets=off, mode="chunk")
+    clean = [h for h in range(H) if h != 3]
+    assert torch.equal(o2[:, clean, :used], o[:, clean, :used]) and torch.equal(S2[:, clean], S[:, clean])
+    assert bool(torch.isnan(o2[0, 3, 75:135]).all()) and bool(torch.isnan(S2[3, 3]).any()) and torch.equal(S2[4], S[4])
+
+
+@pytest.mark.parametrize("scale", [1e-12, 1e12])
+def test_many_heads_at_other_scales(scale):
+    inp = inputs.gdr_inputs(4, 8, 8, 100, 64, 64, "f64", seed=13)
+    for n, f in (("v", scale), ("S0", scale), ("q", 1 / scale)):
+        inp[n] = inp[n] * f
+    t = {n: dev(inp[n], torch.bfloat16) for n in ("q", "k", "v")} | {n: dev(inp[n]) for n in ("g", "beta", "S0")}
+    inp = {n: x.double().cpu().numpy() for n, x in t.items()}
+    o, S = mlstm.gdr_fwd(*(t[n] for n in ("q", "k", "v", "g", "beta", "S0")))
+    o_ref, S_ref = oracle.gdr_sequential(*(inp[n] for n in ("q", "k", "v", "g", "beta", "S0")))
+    close(o, o_ref, "bf16", coarse(inp, "bf16", "chunk"))
+    close(S, S_ref, "f32")
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_workspace_stays_usable():
+    """A limit shorter than any copy takes: the status says so, and an ordinary call on the same workspace is right."""
+    inp = inputs.gdr_inputs(8, 4, 4, 130, 128, 128, "bf16", seed=9)
+    t = to_dev(inp, "bf16")
+    a = [t[n] for n in ("q", "k", "v", "g", "beta", "S0")]
+    short = mlstm.gdr_params(*a[:5], wait_limit_cycles=256)
+    ws = torch.empty(mlstm.gdr_fwd_workspace_size(short), dtype=torch.uint8, device="cuda")
+    mlstm.gdr_fwd(*a, workspace=ws, wait_limit_cycles=256)
+    assert mlstm.gdr_status(short, ws) == 8
+    o, S = mlstm.gdr_fwd(*a, workspace=ws)
+    assert mlstm.gdr_status(mlstm.gdr_params(*a[:5]), ws) == 0
+    o_ref, S_ref = oracle.gdr_sequential(*(inp[n] for n in ("q", "k", "v", "g", "beta", "S0")))
+    close(o, o_ref, "bf16", coarse(inp, "bf16", "chunk"))
+    close(S, S_ref, "f32")
+
+
 def test_no_tokens_and_state_in_place():
     q = torch.empty(2, 1, 0, 16, device="cuda")
     v = torch.empty(2, 2, 0, 8, device="cuda")

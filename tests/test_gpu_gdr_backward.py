@@ -127,9 +127,22 @@ def test_gradients(shape, dtype, states):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_many_heads_take_wider_blocks(dtype):
     """Enough heads for blocks of eight and of four tiles."""
-    for shape in ((8, 16, 16, 70, 64, 72), (10, 5, 10, 66, 128, 64)):
+    for shape in ((8, 16, 16, 70, 64, 72), (10, 5, 10, 66, 128, 64), (4, 4, 8, 130, 128, 128), (2, 8, 16, 65, 40, 136)):
         inp = make(shape, dtype, 5)
         check(call(inp, dtype), inp, dtype)
+
+
+def test_many_heads_packed():
+    lengths, T = (70, 0, 1, 64, 130, 5), 273
+    inp = make((1, 4, 8, T, 64, 48), "bf16", 6, True, len(lengths))
+    offsets = np.concatenate([[0], np.cumsum(lengths)])
+    out = call(inp, "bf16", seq_offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"))
+    for n, x in enumerate(lengths):
+        if x:
+            lo = offsets[n]
+            one = {m: inp[m][:, :, lo:lo + x] for m in NAMES + ("do",)} | {m: inp[m][n:n + 1] for m in ("S0", "dS")}
+            check({m: out[m][:, :, lo:lo + x] for m in ("dq", "dk", "dv", "dg", "dbeta")} | {"dS0": out["dS0"][n:n + 1]},
+                  one, "bf16")
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
