@@ -494,7 +494,8 @@ mlstm_status_t mlstm_step(const mlstm_step_params_t* p,
  *            MLSTM_GDR_CHUNK: chunks of 64 tokens on the tensor cores, a triangular solve per chunk;
  *            K a multiple of 8, at most 128.  Operands are split into 16-bit parts so that states and
  *            gate gradients keep fp32 accuracy.
- *            MLSTM_GDR_AUTO: CHUNK from 32 tokens (T) on where K allows it, else RECURRENT.
+ *            MLSTM_GDR_AUTO: CHUNK from 32 tokens (T) on where K allows it (packed: and 8 a sequence on
+ *            average), else RECURRENT.
  *   V        a multiple of 8
  *   q, k     [B,HK,T,K]  dtype      required (if B, T > 0)
  *   v, o     [B,H,T,V]   dtype      required; o must not overlap an input
@@ -529,8 +530,8 @@ typedef struct {
   mlstm_dtype_t dtype;
   int mode; /* mlstm_gdr_mode_t */
   mlstm_gdr_stride_t q, k, v, g, beta, o;
-  /* Bound of every device-side wait of the tcgen05 pass, in SM cycles; 0 = the default (about two
-   * seconds).  See mlstm_gdr_status. */
+  /* Bound of every device-side wait of mlstm_gdr_fwd's tcgen05 pass, in SM cycles; 0 = the default (about two
+   * seconds).  See mlstm_gdr_status.  Ignored elsewhere. */
   long long wait_limit_cycles;
 } mlstm_gdr_params_t;
 typedef struct {
@@ -552,13 +553,13 @@ mlstm_status_t mlstm_gdr_bwd(const mlstm_gdr_params_t* p, const void* q, const v
                              const float* dS, mlstm_gdr_stride_t s_dq, mlstm_gdr_stride_t s_dk,
                              mlstm_gdr_stride_t s_dv, void* dq, void* dk, void* dv, float* dg, float* dbeta,
                              float* dS0, void* workspace, size_t workspace_bytes, mlstm_stream_t stream);
-/* Outcome of the bounded device-side waits of the last mlstm_gdr_fwd (backward = 0) or mlstm_gdr_bwd
- * (backward = 1) enqueued on `stream` with `workspace` and these params: synchronises `stream`; MLSTM_OK, or
- * MLSTM_ERR_TIMEOUT when a wait of the tcgen05 pass over the chunks (bf16 with many heads) ran out: that
- * call's outputs are unspecified, the workspace can be used again.  MLSTM_OK always for the other paths,
- * which have no such waits.  MLSTM_ERR_CUDA if the synchronisation or the read fails; argument errors as
- * for the call (workspace NULL: MLSTM_ERR_NULL when the tcgen05 pass would run). */
-mlstm_status_t mlstm_gdr_status(const mlstm_gdr_params_t* p, int backward, const void* workspace, mlstm_stream_t stream);
+/* Outcome of the bounded device-side waits of the last mlstm_gdr_fwd enqueued on `stream` with `workspace` and
+ * these params: synchronises `stream`; MLSTM_OK, or MLSTM_ERR_TIMEOUT when a wait of the tcgen05 pass over the
+ * chunks (bf16, wide values, many heads) ran out: that call's outputs are unspecified, the workspace can be
+ * used again.  MLSTM_OK always for the other paths, which have no such waits.  MLSTM_ERR_CUDA if the
+ * synchronisation or the read fails; argument errors as mlstm_gdr_fwd (workspace NULL: MLSTM_ERR_NULL when the
+ * tcgen05 pass would run). */
+mlstm_status_t mlstm_gdr_status(const mlstm_gdr_params_t* p, const void* workspace, mlstm_stream_t stream);
 
 /*
  * Root-mean-square norm of a residual stream (the pre-norm of the xLSTM 7B block) with the residual's

@@ -68,12 +68,13 @@ mlstm_status_t check_gdr(const mlstm_gdr_params_t* p, bool backward, GdrShape* s
   s->unit = 16 / s->es;
   s->N = p->num_seqs > 0 ? p->num_seqs : p->B;
   s->any = p->B > 0 && p->H > 0 && p->T > 0;
+  if ((long long)p->B * p->T > (1LL << 36)) return MLSTM_ERR_SHAPE;  // chunks are counted in 32 bits
   s->chunk = false;
   if (backward || p->mode == MLSTM_GDR_CHUNK) {
     if (!gdr_chunk_supported(p->K)) return MLSTM_ERR_SHAPE;
     s->chunk = true;
   } else if (p->mode == MLSTM_GDR_AUTO) {
-    s->chunk = gdr_chunk_supported(p->K) && p->T >= kGdrChunkFrom;
+    s->chunk = gdr_chunk_supported(p->K) && p->T >= kGdrChunkFrom && p->T >= (long long)kGdrChunkAverage * p->num_seqs;
   }
   if (!strides_ok(p->q, p->B, p->HK, p->T, s->unit) || !strides_ok(p->k, p->B, p->HK, p->T, s->unit) ||
       !strides_ok(p->v, p->B, p->H, p->T, s->unit) || !strides_ok(p->o, p->B, p->H, p->T, s->unit) ||
@@ -248,9 +249,9 @@ mlstm_status_t mlstm_gdr_bwd(const mlstm_gdr_params_t* p, const void* q, const v
   return done(launch_gdr_bwd(a, workspace, (cudaStream_t)stream));
 }
 
-mlstm_status_t mlstm_gdr_status(const mlstm_gdr_params_t* p, int backward, const void* workspace, mlstm_stream_t stream) {
+mlstm_status_t mlstm_gdr_status(const mlstm_gdr_params_t* p, const void* workspace, mlstm_stream_t stream) {
   GdrShape s;
-  mlstm_status_t st = check_gdr(p, backward != 0, &s);
+  mlstm_status_t st = check_gdr(p, false, &s);
   if (st != MLSTM_OK) return st;
   const bool waits = s.chunk && s.any && gdr_tc_pass(gdr_args(p, s));
   if (waits && !workspace) return MLSTM_ERR_NULL;

@@ -490,7 +490,7 @@ BwdLayout bwd_layout(const GdrArgs& a) {
   const size_t nrec = (size_t)record_count(a), tiles = (a.V + 15) / 16;
   const size_t rt = nrec * a.H * tiles, st = (nrec + a.N) * a.H * tiles, key_step = (size_t)(KP / 16) * 512;
   BwdLayout l;
-  size_t at = kGdrHeader + nrec * a.HK * keys_bytes(KP, np);
+  size_t at = nrec * a.HK * keys_bytes(KP, np);
   auto take = [&](size_t n) {
     const size_t here = at;
     at += (n + 255) & ~(size_t)255;
@@ -529,7 +529,7 @@ cudaError_t launch_back(const GdrArgs& a, const char* keys, const char* records,
 template <typename T, int KP>
 cudaError_t backward(const GdrArgs& a, char* ws, cudaStream_t stream) {
   const BwdLayout l = bwd_layout(a);
-  char *keys = ws + kGdrHeader, *records = ws + l.records;
+  char *keys = ws, *records = ws + l.records;
   Kept k;
   k.S = ws + l.S, k.S_inv = (float*)(ws + l.S_inv), k.Z = (float*)(ws + l.Z);
   k.U = ws + l.U, k.U_inv = (float*)(ws + l.U_inv), k.dots = (float*)(ws + l.dots);
@@ -538,12 +538,9 @@ cudaError_t backward(const GdrArgs& a, char* ws, cudaStream_t stream) {
   k.dbeta = (float*)(ws + l.dbeta), k.ends = (float*)(ws + l.ends);
   cudaError_t e = launch_prep<T, KP, true>(a, keys, records, stream);
   if (e != cudaSuccess) return e;
-  bool walked = false;
-  if constexpr (sizeof(T) == 2)
-    if ((walked = gdr_tc_pass(a))) e = launch_tc_walk<KP, true>(a, keys, records, k, (unsigned int*)ws, stream);
-  if (!walked) e = launch_walk<T, KP, true>(a, keys, records, k, stream);
+  e = launch_walk<T, KP, true>(a, keys, records, k, stream);
   if (e != cudaSuccess) return e;
-  const int tn = tiles_a_block<T>(a);
+  const int tn = tiles_a_block(a);
   if constexpr (sizeof(T) == 2)
     if (tn == 4) e = launch_back<T, KP, 4>(a, keys, records, k, stream);
   if (tn != 4) e = tn == 2 ? launch_back<T, KP, 2>(a, keys, records, k, stream) : launch_back<T, KP, 1>(a, keys, records, k, stream);

@@ -184,8 +184,9 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
       }
     }
     __syncthreads();
-    // P, rows scaled, and M; blocks above the diagonal are never read
+    // P, rows scaled, and M, of which blocks above the diagonal are never read
     float p[4][4], big[2] = {0.f, 0.f};
+    zero(p);
     if (lower) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -228,20 +229,18 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
 #pragma unroll
       for (int t = 0; t < 16; ++t) R[(top + t) * kMs + top + lane] = 0.f;
     }
-    if (lower) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = r0 + (lane >> 2) + i * 8;
-        const Scale sc = scale_of(fmaxf(pmax[t], pmax[kL + t]));
-        if (c0 == 0 && (lane & 3) == 0) fac[kPInv * kL + t] = sc.inv;
+    for (int i = 0; i < 2; ++i) {
+      const int t = r0 + (lane >> 2) + i * 8;
+      const Scale sc = scale_of(fmaxf(pmax[t], pmax[kL + t]));
+      if (c0 == 0 && (lane & 3) == 0) fac[kPInv * kL + t] = sc.inv;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t hi, lo;
-          split(p[j][2 * i] * sc.mul, p[j][2 * i + 1] * sc.mul, hi, lo);
-          char* at = out + 2 * kTile + piece_at<kL>(t, c0 + j * 8) + (lane & 3) * 4;
-          *reinterpret_cast<uint32_t*>(at) = hi;
-          if constexpr (P2) *reinterpret_cast<uint32_t*>(at + kTile) = lo;
-        }
+      for (int j = 0; j < 4; ++j) {
+        uint32_t hi, lo;
+        split(p[j][2 * i] * sc.mul, p[j][2 * i + 1] * sc.mul, hi, lo);
+        char* at = out + 2 * kTile + piece_at<kL>(t, c0 + j * 8) + (lane & 3) * 4;
+        *reinterpret_cast<uint32_t*>(at) = hi;
+        if constexpr (P2) *reinterpret_cast<uint32_t*>(at + kTile) = lo;
       }
     }
     __syncthreads();
@@ -255,7 +254,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
       join_half<32>(half, M, R, X, beta, 0, warp >> 2, warp & 3, lane);
       __syncthreads();
     }
-    {  // R, rows scaled: four threads a row, 16 columns each, none above the diagonal's block
+    {  // R, rows scaled: four threads a row, 16 columns each, zeros above the diagonal's block
       const int row = tid >> 2, part = tid & 3;
       const bool below = part * 16 <= row;
       float x[16], m = 0.f;
@@ -270,16 +269,14 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const Scale sc = scale_of(m);
       if (part == 0) fac[kRInv * kL + row] = sc.inv;
-      if (below) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t hi[4], lo[4];
+      for (int i = 0; i < 2; ++i) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) split(x[i * 8 + 2 * e] * sc.mul, x[i * 8 + 2 * e + 1] * sc.mul, hi[e], lo[e]);
-          const int at = piece_at<kL>(row, part * 16 + i * 8);
-          *reinterpret_cast<uint4*>(out + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(out + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
+        for (int e = 0; e < 4; ++e) split(x[i * 8 + 2 * e] * sc.mul, x[i * 8 + 2 * e + 1] * sc.mul, hi[e], lo[e]);
+        const int at = piece_at<kL>(row, part * 16 + i * 8);
+        *reinterpret_cast<uint4*>(out + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(out + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
     __syncthreads();
@@ -315,7 +312,7 @@ cudaError_t chunk(const GdrArgs& a, char* ws, cudaStream_t stream) {
   cudaError_t e = launch_prep<T, KP, P2>(a, keys, records, stream);
   if (e != cudaSuccess) return e;
   if constexpr (sizeof(T) == 2)
-    if (gdr_tc_pass(a)) return launch_tc_walk<KP, false>(a, keys, records, Kept{}, (unsigned int*)ws, stream);
+    if (gdr_tc_pass(a)) return launch_tc_walk<KP>(a, keys, records, (unsigned int*)ws, stream);
   return launch_walk<T, KP, false>(a, keys, records, Kept{}, stream);
 }
 
@@ -324,7 +321,10 @@ cudaError_t chunk(const GdrArgs& a, char* ws, cudaStream_t stream) {
 
 bool gdr_chunk_supported(int K) { return K <= 128; }
 
-bool gdr_tc_pass(const GdrArgs& a) { return a.dtype == 1 && a.V > 32 && (long long)a.N * a.H * ((a.V + 127) / 128) >= 32; }
+// bf16 inputs: whichever pass takes less (walk_cost).
+bool gdr_tc_pass(const GdrArgs& a) {
+  return a.dtype == 1 && gdr::walk_cost(a, 0) < gdr::walk_cost(a, gdr::tiles_a_block(a));
+}
 
 size_t gdr_chunk_workspace_bytes(const GdrArgs& a) {
   const int np = a.dtype ? 1 : 2, KP = a.K <= 64 ? 64 : 128;

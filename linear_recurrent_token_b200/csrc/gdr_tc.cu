@@ -4,12 +4,13 @@
 // One block takes up to 128 value columns of one value head of one sequence.  Tensor memory has a lane for
 // each value column: the state's, Z's and U's 16-bit parts are A operands there, k, q, R and P are B
 // operands in shared memory, and every product has M = 128.  The state itself stays in the registers of
-// eight warps (a lane is a column, two warps share its keys); each chunk's update is summed from zero in
-// tensor memory and added in fp32.  A chunk is one chain:
+// eight warps (a lane is a column, two warps share its keys and tokens); each chunk's update is summed
+// from zero in tensor memory and added in fp32.  A chunk is one chain:
 //     S in parts -> K S, Q S -> Z -> R (beta Z) -> Z', U -> (w K)^T U -> S
 // with the copies of the next chunk, Q S and P U beside it; the output is written while the update runs.  It is bound by that chain: the
-// four products take about 1600 cycles of it for 128 keys and columns, the rest is what the eight warps do
-// between them.
+// four products take about 1700 cycles of it for 128 keys and columns, the rest is what the eight warps do
+// between them (9100 cycles a chunk in all; sixteen warps, four to a scheduler, took 10700: the chain waits
+// for latencies, not for issue slots).
 #include "gdr_walk.cuh"
 #include "sm100.cuh"
 
@@ -48,17 +49,17 @@ struct TcBars {
   uint64_t full[2], empty[2], s_ready, x_full, z_ready, r_full, u_ready, o_full, d_full, drain;
 };
 
-template <int KP, bool GRAD>
+template <int KP>
 struct TcStage {
   static constexpr int q = keys_bytes(KP, 1) / 2;
   static constexpr int record = keys_bytes(KP, 1);
   static constexpr int p = record + 2 * kTile;
-  static constexpr int factors = record + record_bytes(GRAD) - kFactorBytes;
-  static constexpr int v = record + record_bytes(GRAD);  // [64][128]
-  static constexpr int dout = v + kL * 256;
-  static constexpr int bytes = dout + (GRAD ? kL * 256 : 0);
-  // behind two stages: maxima in exchange [4][2 halves][128]
-  static constexpr int ex = 2 * bytes;
+  static constexpr int factors = record + record_bytes(false) - kFactorBytes;
+  static constexpr int v = record + record_bytes(false);  // [64][128]
+  static constexpr int bytes = v + kL * 256;
+  // behind two stages: the output on its way to memory [64 tokens][136], the maxima in exchange [4][2][128]
+  static constexpr int out = 2 * bytes;
+  static constexpr int ex = out + kL * 272;
   static constexpr int bars = ex + 4 * 2 * 128 * 4;
   static constexpr int total = bars + (int)sizeof(TcBars) + 1024;  // and the slack of aligning the base to 1 KB
   static_assert(bytes % 1024 == 0 && total <= 227 * 1024, "a block's shared memory");
@@ -72,35 +73,23 @@ __device__ __noinline__ bool tc_wait_slow(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ float max16(float m) {  // over the 16 lanes of a tile
+// 2 N values times f as two parts: N words each.
+template <int N>
+__device__ __forceinline__ void split_words(const float* x, float f, float (&hi)[N], float (&lo)[N]) {
 #pragma unroll
-  for (int d = 8; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  return m;
-}
-
-// 32 values times f as two parts: 16 words each.
-__device__ __forceinline__ void split32(const float* x, float f, float (&hi)[16], float (&lo)[16]) {
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < N; ++j) {
     uint32_t h, l;
     split(x[2 * j] * f, x[2 * j + 1] * f, h, l);
     hi[j] = __uint_as_float(h), lo[j] = __uint_as_float(l);
   }
 }
-// 32 columns from c0 of row r of a kept tile
-template <int COLS>
-__device__ __forceinline__ void keep_row(char* tile, int r, int c0, const float (&w)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<float4*>(tile + piece_at<COLS, 16>(r, c0 + 8 * i)) =
-        make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-}
+__device__ __forceinline__ void st_words(uint32_t at, const float (&w)[16]) { tmem_st16(at, w); }
 
-template <int KP, bool GRAD>
+template <int KP>
 __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, const char* keys, const char* records,
-                                                               const Kept kept, unsigned int* err, long long limit) {
-  using L = TcStage<KP, GRAD>;
-  constexpr int KH = KP / 2;
+                                                               unsigned int* err, long long limit) {
+  using L = TcStage<KP>;
+  constexpr int KH = KP / 2, TH = kL / 2;  // keys and tokens of a value warp
   extern __shared__ uint8_t raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   float* ex = reinterpret_cast<float*>(sm + L::ex);
@@ -135,24 +124,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
   if (warp == 0) {
     // ------------------------------------------------------------------------------------ producer
     const char* kq = keys + (s.slot * a.HK + h / (a.H / a.HK)) * keys_bytes(KP, 1);
-    const char* rec = records + (s.slot * a.H + h) * record_bytes(GRAD);
+    const char* rec = records + (s.slot * a.H + h) * record_bytes(false);
     const int width = min(128, a.V - v0) * 2;  // bytes of a row of v: a multiple of 16
     const __nv_bfloat16* v = (const __nv_bfloat16*)a.v + s.b * a.sv.b + h * a.sv.h + s.lo * a.sv.t + v0;
-    const __nv_bfloat16* d = GRAD ? (const __nv_bfloat16*)a.dout + s.b * a.so.b + h * a.so.h + s.lo * a.so.t + v0 : nullptr;
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, rows = (int)min((long long)kL, s.len - (long long)c * kL);
       if (!wait(&bars.empty[b], ((c >> 1) & 1) ^ 1)) break;
       uint8_t* st = sm + b * L::bytes;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&bars.full[b], keys_bytes(KP, 1) + record_bytes(GRAD) + (GRAD ? 2 : 1) * rows * width);
+        mbar_arrive_expect_tx(&bars.full[b], keys_bytes(KP, 1) + record_bytes(false) + rows * width);
         sm100::bulk_load(st, kq + (long long)c * a.HK * keys_bytes(KP, 1), keys_bytes(KP, 1), &bars.full[b]);
-        sm100::bulk_load(st + L::record, rec + (long long)c * a.H * record_bytes(GRAD), record_bytes(GRAD), &bars.full[b]);
+        sm100::bulk_load(st + L::record, rec + (long long)c * a.H * record_bytes(false), record_bytes(false), &bars.full[b]);
       }
       __syncwarp();
       for (int t = lane; t < rows; t += 32) {
         const long long at = (long long)c * kL + t;
         sm100::bulk_load(st + L::v + t * 256, v + at * a.sv.t, width, &bars.full[b]);
-        if (GRAD) sm100::bulk_load(st + L::dout + t * 256, d + at * a.so.t, width, &bars.full[b]);
       }
       issued = c + 1;
       __syncwarp();
@@ -161,20 +148,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
     // ------------------------------------------------------------------------------------ products
     bool ok = true;
     // D (+)= A B over the 16-column steps of the state, A's part at column `at`, B's keys at `bd`
-    auto by_state = [&](uint32_t d, uint32_t at, uint64_t bd, uint32_t more) {
-#pragma unroll 1
-      for (int k = 0; k < KP / 16; ++k) {
-        mma_bf16_ts(d, at + 8 * k, bd + (uint64_t)((k >> 2) * 512 + (k & 3) * 2), idesc_f16(64, 0), more);
-        more = 1u;
-      }
+    auto by_state = [&](uint32_t d, uint32_t at, uint64_t bd, bool more) {
+#pragma unroll
+      for (int k = 0; k < KP / 16; ++k)
+        mma_bf16_ts(d, at + 8 * k, bd + (uint64_t)((k >> 2) * 512 + (k & 3) * 2), idesc_f16(64, 0), more || k > 0 ? 1u : 0u);
     };
-    // the same over the tokens of a lower triangular B: the k step of tokens 16 kk .. reaches rows from 16 kk on
-    auto by_tokens_of = [&](uint32_t d, uint32_t at, uint64_t bd, uint32_t more) {
-#pragma unroll 1
-      for (int kk = 0; kk < 4; ++kk) {
-        mma_bf16_ts(d + 16 * kk, at + 8 * kk, bd + (uint64_t)(kk * 130), idesc_f16(64, 0) - ((uint32_t)(2 * kk) << 17), more);
-        more = 1u;
-      }
+    // the same over the tokens of R or P
+    auto by_tokens_of = [&](uint32_t d, uint32_t at, uint64_t bd, bool more) {
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_bf16_ts(d, at + 8 * kk, bd + (uint64_t)(kk * 2), idesc_f16(64, 0), more || kk > 0 ? 1u : 0u);
     };
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1;
@@ -184,11 +167,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
       tc_fence_after();
       if (elect_one()) {  // lo parts first: they are small, and so is what the sums cut off below them
         const uint64_t kd = smem_desc_sw128(st, 16, 1024), qd = smem_desc_sw128(st + L::q, 16, 1024);
-        by_state(tm + kTmX, tm + kTmS + KP / 2, kd, 0u);
-        by_state(tm + kTmX, tm + kTmS, kd, 1u);
+        by_state(tm + kTmX, tm + kTmS + KP / 2, kd, false);
+        by_state(tm + kTmX, tm + kTmS, kd, true);
         mma_commit(&bars.x_full);
-        if (GRAD) by_state(tm + kTmO, tm + kTmS + KP / 2, qd, 0u);
-        by_state(tm + kTmO, tm + kTmS, qd, GRAD ? 1u : 0u);
+        by_state(tm + kTmO, tm + kTmS, qd, false);  // one part (11 bits) for an output in bf16
       }
       __syncwarp();
       ok = wait(&bars.z_ready, c & 1);
@@ -196,9 +178,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
       tc_fence_after();
       if (elect_one()) {
         const uint64_t rd = smem_desc_sw128(st + L::record, 16, 1024);
-        by_tokens_of(tm + kTmX, tm + kTmZ + 32, rd, 0u);
-        by_tokens_of(tm + kTmX, tm + kTmZ, rd + (kTile >> 4), 1u);
-        by_tokens_of(tm + kTmX, tm + kTmZ, rd, 1u);
+        by_tokens_of(tm + kTmX, tm + kTmZ + 32, rd, false);
+        by_tokens_of(tm + kTmX, tm + kTmZ, rd + (kTile >> 4), true);
+        by_tokens_of(tm + kTmX, tm + kTmZ, rd, true);
         mma_commit(&bars.r_full);
       }
       __syncwarp();
@@ -207,13 +189,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
       tc_fence_after();
       if (elect_one()) {
         const uint64_t kmn = smem_desc_sw128(st, 8192, 1024), pd = smem_desc_sw128(st + L::p, 16, 1024);
-        if (GRAD) {
-          by_tokens_of(tm + kTmX, tm + kTmU + 32, pd, 0u);
-          by_tokens_of(tm + kTmX, tm + kTmU, pd + (kTile >> 4), 1u);
-        }
-        by_tokens_of(tm + kTmX, tm + kTmU, pd, GRAD ? 1u : 0u);
+        by_tokens_of(tm + kTmX, tm + kTmU, pd, false);
         mma_commit(&bars.o_full);
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < 8; ++i)  // w U's second part, then its first
           mma_bf16_ts(tm + kTmD, tm + kTmZ + (i < 4 ? 32 : 0) + 8 * (i & 3), kmn + (uint64_t)((i & 3) * 128), idesc_f16(KP, 1),
                       i > 0 ? 1u : 0u);
@@ -231,87 +209,97 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
     const bool live = v < a.V;
     const uint32_t ln = tm + ((uint32_t)(32 * q4) << 16);
     const size_t state = ((size_t)n * a.H + h) * a.K * a.V + v;
-    const int tiles = (a.V + 15) / 16, tile = v >> 4, tr = v & 15;
-    const bool tile_live = tile < tiles;
-    const int t0 = 32 * half;
+    const int t0 = TH * half, k0 = KH * half;
     float S[KH];
 #pragma unroll
-    for (int j = 0; j < KH; ++j)
-      S[j] = a.S0 && live && half * KH + j < a.K ? a.S0[state + (size_t)(half * KH + j) * a.V] : 0.f;
-    // the larger of the two warps' maxima of a column (of a tile for the gradients, whose products sum over columns)
-    auto agree = [&](int which, float m) {
-      if (GRAD) m = max16(m);
-      ex[(which * 2 + half) * 128 + col] = m;
-      return m;
-    };
-    auto other = [&](int which) { return ex[(which * 2 + 1 - half) * 128 + col]; };
-    auto keep_state = [&](long long number, const Scale& sc, int blk, const float (&hi)[16], const float (&lo)[16]) {
-      if (!GRAD || !tile_live) return;
-      const size_t base = ((size_t)number * a.H + h) * tiles + tile;
-      char* at = kept.S + base * 2 * 16 * KP * 2;
-      keep_row<KP>(at, tr, half * KH + 32 * blk, hi);
-      keep_row<KP>(at + 16 * KP * 2, tr, half * KH + 32 * blk, lo);
-      if (tr == 0 && half == 0 && blk == 0)
-        *reinterpret_cast<float4*>(kept.S_inv + base * kQuarter) = make_float4(sc.inv, sc.inv, sc.inv, sc.inv);
+    for (int j = 0; j < KH; ++j) S[j] = a.S0 && live && k0 + j < a.K ? a.S0[state + (size_t)(k0 + j) * a.V] : 0.f;
+    // The larger of the two warps' maxima of a column: each gives its own, they meet, and each takes both.
+    auto give_max = [&](int which, float m) { ex[(which * 2 + half) * 128 + col] = m; };
+    auto meet = [&] { named_bar(1 + q4, 64); };
+    auto take_max = [&](int which) { return fmaxf(ex[which * 256 + col], ex[which * 256 + 128 + col]); };
+    auto max4 = [](float m, const float* x) {
+      return fmaxf(fmaxf(m, fmaxf(fabsf(x[0]), fabsf(x[1]))), fmaxf(fabsf(x[2]), fabsf(x[3])));
     };
     auto state_scale = [&] {
       float m = 0.f;
 #pragma unroll
-      for (int j = 0; j < KH; ++j) m = fmaxf(m, fabsf(S[j]));
-      m = agree(0, m);
-      named_bar(1 + q4, 64);
-      return scale_of(fmaxf(m, other(0)));
+      for (int j = 0; j < KH; j += 4) m = max4(m, S + j);
+      give_max(0, m);
+      meet();
+      return scale_of(take_max(0));
     };
+    // The output of a chunk, two tokens a word, leaves by way of shared memory: rows of this warp's 32 columns.
+    uint32_t y[TH / 2];
+    char* mine = reinterpret_cast<char*>(sm + L::out) + t0 * 272 + q4 * 64;
+    auto write_out = [&](int c) {
+#pragma unroll
+      for (int j = 0; j < TH / 2; ++j) {
+        *reinterpret_cast<uint16_t*>(mine + 2 * j * 272 + lane * 2) = (uint16_t)y[j];
+        *reinterpret_cast<uint16_t*>(mine + (2 * j + 1) * 272 + lane * 2) = (uint16_t)(y[j] >> 16);
+      }
+      __syncwarp();
+      const int len = (int)min((long long)kL, s.len - (long long)c * kL), piece = lane & 3, first = v0 + 32 * q4 + 8 * piece;
+      __nv_bfloat16* o = (__nv_bfloat16*)a.o + s.b * a.so.b + h * a.so.h + (s.lo + (long long)c * kL + t0) * a.so.t + first;
+#pragma unroll
+      for (int i = 0; i < TH / 8; ++i) {
+        const int t = i * 8 + (lane >> 2);
+        if (first < a.V && t0 + t < len)
+          *reinterpret_cast<uint4*>(o + t * a.so.t) = *reinterpret_cast<const uint4*>(mine + t * 272 + piece * 16);
+      }
+      __syncwarp();
+    };
+    auto at4 = [](const float* f, int t) { return *reinterpret_cast<const float4*>(f + t); };
     for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, len = (int)min((long long)kL, s.len - (long long)c * kL);
-      const long long rec = s.slot + c;
-      const size_t base = ((size_t)rec * a.H + h) * tiles + tile;
       const uint8_t* st = sm + b * L::bytes;
-      const float* fac = reinterpret_cast<const float*>(st + L::factors);
+      const float* fac = reinterpret_cast<const float*>(st + L::factors) + t0;
       const Scale ss = state_scale();  // (both warps have the update before: its columns may be written again)
 #pragma unroll
-      for (int blk = 0; blk < KH / 32; ++blk) {
+      for (int i = 0; i < KH; i += 32) {
         float hi[16], lo[16];
-        split32(S + 32 * blk, ss.mul, hi, lo);
-        tmem_st16(ln + kTmS + half * (KH / 2) + 16 * blk, hi);
-        tmem_st16(ln + kTmS + KP / 2 + half * (KH / 2) + 16 * blk, lo);
-        keep_state(rec + n, ss, blk, hi, lo);
+        split_words(S + i, ss.mul, hi, lo);
+        st_words(ln + kTmS + (k0 + i) / 2, hi);
+        st_words(ln + kTmS + KP / 2 + (k0 + i) / 2, lo);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.s_ready);
+      if (c > 0) write_out(c - 1);  // beside K S
 
       // Z = V - gam (K S)
       wait(&bars.full[b], (c >> 1) & 1);
-      wait(&bars.x_full, c & 1);
-      tc_fence_after();
-      float z[32], m = 0.f;
-      tmem_ld32(ln + kTmX + t0, z);
-      tmem_wait_ld();
-      const __nv_bfloat16* vt = reinterpret_cast<const __nv_bfloat16*>(st + L::v) + col;
+      float z[TH], u[TH], m = 0.f;
+      {
+        const __nv_bfloat16* vt = reinterpret_cast<const __nv_bfloat16*>(st + L::v) + t0 * 128 + col;
+        if (len == kL && v0 + 128 <= a.V) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 gk = *reinterpret_cast<const float4*>(fac + kGK * kL + t0 + j);
-        const float4 be = *reinterpret_cast<const float4*>(fac + kBeta * kL + t0 + j);
-        const float g4[4] = {gk.x, gk.y, gk.z, gk.w}, b4[4] = {be.x, be.y, be.z, be.w};
+          for (int j = 0; j < TH; ++j) u[j] = __bfloat162float(vt[j * 128]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = live && t0 + j + e < len ? __bfloat162float(vt[(t0 + j + e) * 128]) : 0.f;
-          z[j + e] = fmaf(-g4[e] * ss.inv, z[j + e], x);
-          m = fmaxf(m, fabsf(b4[e] * z[j + e]));
+          for (int j = 0; j < TH; ++j) u[j] = live && t0 + j < len ? __bfloat162float(vt[j * 128]) : 0.f;
         }
       }
-      m = agree(1, m);
-      named_bar(1 + q4, 64);
-      const Scale sz = scale_of(fmaxf(m, other(1)));
-      {
-        float x[32], hi[16], lo[16];
+      wait(&bars.x_full, c & 1);
+      tc_fence_after();
+      tmem_ld32(ln + kTmX + t0, z);
+      tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = fac[kBeta * kL + t0 + j] * z[j];
-        split32(x, sz.mul, hi, lo);
-        tmem_st16(ln + kTmZ + 16 * half, hi);
-        tmem_st16(ln + kTmZ + 32 + 16 * half, lo);
+      for (int j = 0; j < TH; j += 4) {
+        const float4 gk = at4(fac + kGK * kL, j), be = at4(fac + kBeta * kL, j);
+        z[j] = fmaf(-gk.x * ss.inv, z[j], u[j]), z[j + 1] = fmaf(-gk.y * ss.inv, z[j + 1], u[j + 1]);
+        z[j + 2] = fmaf(-gk.z * ss.inv, z[j + 2], u[j + 2]), z[j + 3] = fmaf(-gk.w * ss.inv, z[j + 3], u[j + 3]);
+        u[j] = be.x * z[j], u[j + 1] = be.y * z[j + 1], u[j + 2] = be.z * z[j + 2], u[j + 3] = be.w * z[j + 3];
+        m = max4(m, u + j);
+      }
+      give_max(1, m);
+      meet();
+      const Scale sz = scale_of(take_max(1));
+      {
+        float hi[TH / 2], lo[TH / 2];
+        split_words(u, sz.mul, hi, lo);
+        st_words(ln + kTmZ + t0 / 2, hi);
+        st_words(ln + kTmZ + 32 + t0 / 2, lo);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -321,49 +309,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
       // Z' = Z + R (beta Z), U = beta Z', w U
       wait(&bars.r_full, c & 1);
       tc_fence_after();
-      float u[32], mu = 0.f, mw = 0.f;
+      float mu = 0.f, mw = 0.f;
       tmem_ld32(ln + kTmX + t0, u);
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 ri = *reinterpret_cast<const float4*>(fac + kRInv * kL + t0 + j);
-        const float4 be = *reinterpret_cast<const float4*>(fac + kBeta * kL + t0 + j);
-        const float4 wk = *reinterpret_cast<const float4*>(fac + kWK * kL + t0 + j);
-        const float r4[4] = {ri.x, ri.y, ri.z, ri.w}, b4[4] = {be.x, be.y, be.z, be.w}, w4[4] = {wk.x, wk.y, wk.z, wk.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          z[j + e] = fmaf(u[j + e] * sz.inv, r4[e], z[j + e]);
-          u[j + e] = b4[e] * z[j + e];
-          mu = fmaxf(mu, fabsf(u[j + e]));
-          mw = fmaxf(mw, fabsf(w4[e] * u[j + e]));
-        }
+      for (int j = 0; j < TH; j += 4) {
+        const float4 ri = at4(fac + kRInv * kL, j), be = at4(fac + kBeta * kL, j), wk = at4(fac + kWK * kL, j);
+        z[j] = fmaf(u[j], ri.x * sz.inv, z[j]), z[j + 1] = fmaf(u[j + 1], ri.y * sz.inv, z[j + 1]);
+        z[j + 2] = fmaf(u[j + 2], ri.z * sz.inv, z[j + 2]), z[j + 3] = fmaf(u[j + 3], ri.w * sz.inv, z[j + 3]);
+        u[j] = be.x * z[j], u[j + 1] = be.y * z[j + 1], u[j + 2] = be.z * z[j + 2], u[j + 3] = be.w * z[j + 3];
+        z[j] = wk.x * u[j], z[j + 1] = wk.y * u[j + 1], z[j + 2] = wk.z * u[j + 2], z[j + 3] = wk.w * u[j + 3];
+        mu = max4(mu, u + j);
+        mw = max4(mw, z + j);
       }
-      if (GRAD && tile_live) {
-        float4* at = reinterpret_cast<float4*>(kept.Z + (base * 16 + tr) * kL + t0);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) at[j] = make_float4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
-      }
-      mu = agree(2, mu);
-      mw = agree(3, mw);
-      named_bar(1 + q4, 64);
-      const Scale su = scale_of(fmaxf(mu, other(2))), sw = scale_of(fmaxf(mw, other(3)));
+      give_max(2, mu);
+      give_max(3, mw);
+      meet();
+      const Scale su = scale_of(take_max(2)), sw = scale_of(take_max(3));
       {
-        float hi[16], lo[16];
-        split32(u, su.mul, hi, lo);
-        tmem_st16(ln + kTmU + 16 * half, hi);
-        if (GRAD) tmem_st16(ln + kTmU + 32 + 16 * half, lo);
-        if (GRAD && tile_live) {
-          keep_row<kL>(kept.U + base * 16 * kL * 2, tr, t0, hi);
-          if (tr == 0 && half == 0)
-            *reinterpret_cast<float4*>(kept.U_inv + base * kQuarter) = make_float4(su.inv, su.inv, su.inv, su.inv);
-        }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) u[j] *= fac[kWK * kL + t0 + j];
-        split32(u, sw.mul, hi, lo);
-        tmem_st16(ln + kTmZ + 16 * half, hi);
-        tmem_st16(ln + kTmZ + 32 + 16 * half, lo);
+        float hi[TH / 2], lo[TH / 2];
+        split_words(u, su.mul, hi, lo);
+        st_words(ln + kTmU + t0 / 2, hi);
+        split_words(z, sw.mul, hi, lo);
+        st_words(ln + kTmZ + t0 / 2, hi);
+        st_words(ln + kTmZ + 32 + t0 / 2, lo);
       }
-      const float keep = fac[kGam * kL + kL - 1];
+      const float keep = fac[kGam * kL + kL - 1 - t0];
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -376,34 +347,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
       tmem_ld32(ln + kTmX + t0, u);
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 gq = *reinterpret_cast<const float4*>(fac + kGQ * kL + t0 + j);
-        const float4 pi = *reinterpret_cast<const float4*>(fac + kPInv * kL + t0 + j);
-        const float g4[4] = {gq.x, gq.y, gq.z, gq.w}, p4[4] = {pi.x, pi.y, pi.z, pi.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[j + e] = fmaf(g4[e] * ss.inv, z[j + e], p4[e] * su.inv * u[j + e]);
+      for (int j = 0; j < TH; j += 4) {
+        const float4 gq = at4(fac + kGQ * kL, j), pi = at4(fac + kPInv * kL, j);
+        u[j] = fmaf(gq.x * ss.inv, z[j], pi.x * su.inv * u[j]);
+        u[j + 1] = fmaf(gq.y * ss.inv, z[j + 1], pi.y * su.inv * u[j + 1]);
+        u[j + 2] = fmaf(gq.z * ss.inv, z[j + 2], pi.z * su.inv * u[j + 2]);
+        u[j + 3] = fmaf(gq.w * ss.inv, z[j + 3], pi.w * su.inv * u[j + 3]);
       }
-      if constexpr (GRAD) {  // dO . O over the 16 columns of a tile: lane l of 16 ends with tokens 2 l, 2 l + 1
-        const __nv_bfloat16* dt = reinterpret_cast<const __nv_bfloat16*>(st + L::dout) + col;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) u[j] = live && t0 + j < len ? u[j] * __bfloat162float(dt[(t0 + j) * 128]) : 0.f;
-#pragma unroll
-        for (int w = 16; w > 1; w /= 2) {
-          const bool up = lane & (w / 2);
-#pragma unroll
-          for (int i = 0; i < w; ++i) {
-            const float mine = up ? u[i + w] : u[i], theirs = up ? u[i] : u[i + w];
-            u[i] = mine + __shfl_xor_sync(0xffffffffu, theirs, w / 2);
-          }
-        }
-        if (tile_live)
-          *reinterpret_cast<float2*>(kept.dots + base * kL + t0 + 2 * (lane & 15)) = make_float2(u[0], u[1]);
-      } else if (live) {
-        __nv_bfloat16* out = (__nv_bfloat16*)a.o + s.b * a.so.b + h * a.so.h + (s.lo + (long long)c * kL + t0) * a.so.t + v;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (t0 + j < len) out[j * a.so.t] = __float2bfloat16_rn(u[j]);
-      }
+      for (int j = 0; j < TH / 2; ++j) y[j] = pack_bf16(u[2 * j], u[2 * j + 1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.empty[b]);
 
@@ -411,27 +363,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
       wait(&bars.d_full, c & 1);
       tc_fence_after();
 #pragma unroll
-      for (int blk = 0; blk < KH / 32; ++blk) {
+      for (int i = 0; i < KH; i += 32) {
         float d[32];
-        tmem_ld32(ln + kTmD + half * KH + 32 * blk, d);
+        tmem_ld32(ln + kTmD + k0 + i, d);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[32 * blk + j] = fmaf(keep, S[32 * blk + j], sw.inv * d[j]);
+        for (int j = 0; j < 32; ++j) S[i + j] = fmaf(keep, S[i + j], sw.inv * d[j]);
       }
     }
-    if constexpr (GRAD) {
-      const Scale ss = state_scale();
-#pragma unroll
-      for (int blk = 0; blk < KH / 32; ++blk) {
-        float hi[16], lo[16];
-        split32(S + 32 * blk, ss.mul, hi, lo);
-        keep_state(s.slot + chunks + n, ss, blk, hi, lo);
-      }
-    }
+    if (chunks > 0) write_out(chunks - 1);
     if (a.S_out && live)
 #pragma unroll
       for (int j = 0; j < KH; ++j)
-        if (half * KH + j < a.K) a.S_out[state + (size_t)(half * KH + j) * a.V] = S[j];
+        if (k0 + j < a.K) a.S_out[state + (size_t)(k0 + j) * a.V] = S[j];
   }
 
   // drain before tensor memory is freed: every product issued has completed and every copy has landed (the
@@ -455,21 +399,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
 
 }  // namespace
 
-template <int KP, bool GRAD>
-cudaError_t launch_tc_walk(const GdrArgs& a, const char* keys, const char* records, const Kept& kept, unsigned int* err,
-                           cudaStream_t stream) {
-  constexpr int smem = TcStage<KP, GRAD>::total;
-  const auto kernel = gdr_tc_kernel<KP, GRAD>;
+template <int KP>
+cudaError_t launch_tc_walk(const GdrArgs& a, const char* keys, const char* records, unsigned int* err, cudaStream_t stream) {
+  constexpr int smem = TcStage<KP>::total;
+  const auto kernel = gdr_tc_kernel<KP>;
   cudaError_t e = cudaMemsetAsync(err, 0, 64, stream);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3((a.V + 127) / 128, a.H, a.N), kTcThreads, smem, stream>>>(a, keys, records, kept, err, a.wait);
+  kernel<<<dim3((a.V + 127) / 128, a.H, a.N), kTcThreads, smem, stream>>>(a, keys, records, err, a.wait);
   return cudaGetLastError();
 }
-template cudaError_t launch_tc_walk<64, false>(const GdrArgs&, const char*, const char*, const Kept&, unsigned int*, cudaStream_t);
-template cudaError_t launch_tc_walk<128, false>(const GdrArgs&, const char*, const char*, const Kept&, unsigned int*, cudaStream_t);
-template cudaError_t launch_tc_walk<64, true>(const GdrArgs&, const char*, const char*, const Kept&, unsigned int*, cudaStream_t);
-template cudaError_t launch_tc_walk<128, true>(const GdrArgs&, const char*, const char*, const Kept&, unsigned int*, cudaStream_t);
+template cudaError_t launch_tc_walk<64>(const GdrArgs&, const char*, const char*, unsigned int*, cudaStream_t);
+template cudaError_t launch_tc_walk<128>(const GdrArgs&, const char*, const char*, unsigned int*, cudaStream_t);
 
 }  // namespace gdr
 }  // namespace mlstm

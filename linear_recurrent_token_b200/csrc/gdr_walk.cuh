@@ -1,6 +1,7 @@
 // The pass over a sequence's chunks: forward for outputs and states, or again for the gradients, which
 // keep what they need of it.
 #pragma once
+#include <algorithm>
 
 #include "gdr_tile.cuh"
 
@@ -32,9 +33,8 @@ struct Kept {
 template <typename T>
 constexpr int kept_parts() { return sizeof(T) == 4 ? 2 : 1; }
 
-template <int KP, bool GRAD>
-cudaError_t launch_tc_walk(const GdrArgs& a, const char* keys, const char* records, const Kept& kept, unsigned int* err,
-                           cudaStream_t stream);
+template <int KP>
+cudaError_t launch_tc_walk(const GdrArgs& a, const char* keys, const char* records, unsigned int* err, cudaStream_t stream);
 template <typename T, int KP, bool P2>
 cudaError_t launch_prep(const GdrArgs& a, char* keys, char* records, cudaStream_t stream);
 
@@ -429,12 +429,36 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_walk_kernel(const GdrA
   }
 }
 
-// Tiles a block: as many as fit, fewer while the blocks do not fill the SMs.
-template <typename T>
-int tiles_a_block(const GdrArgs& a) {
-  const long long heads = (long long)a.N * a.H, tiles = (a.V + 15) / 16;
-  if (sizeof(T) == 2 && tiles > 2 && heads * ((tiles + 3) / 4) >= 100) return 4;
-  return tiles > 1 && heads * ((tiles + 1) / 2) >= 100 ? 2 : 1;
+// What a pass over 32 chunks would take with blocks of 16 TN columns (TN = 0: the tcgen05 pass, 128 columns), in
+// us.  A block's chunks are one chain, longer the more columns it has; blocks beyond the 148 SMs make a
+// further round of it.  For bf16 keys of up to 64 two blocks of one or two tiles share an SM and each other's
+// waits.  Sequences of one length go round in whole rounds; packed ones are uneven (their lengths are not known on
+// the host): shorter ones make room, so count half of them, and no fewer than the longest one's chain.
+// The chains are measured (T = 2048, one block an SM: 80, 105, 160, 165 us for 128 keys; 72, 95, 140, 165
+// for 64), and so is what follows from them; us with the preparation, TN = 1 / 2 / 4 / tcgen05:
+//   128 x 128, 16 heads 106/133/188/194, 32: 196/153/208/215, 64: 371/286/245/250, 80: 458/402/416/268,
+//   128: 657/557/474/327, 256: 1294/999/926/633;   128 x 256, 32 heads 336/252/210/219, 48: 493/366/381/238
+//   64 x 64, 16 heads 90/108/145/178, 64: 156/154/189/227, 128: 295/259/255/295, 256: 565/498/493/560
+//   64 x 128, 32 heads 126/123/161/187, 64: 230/195/191/218, 80: 319/282/320/231, 128: 446/376/372/280
+//   64 x 128 packed, 13 uneven sequences of 6007 tokens, 4 heads 82/103/102/121, 8: 114/116/116/129, 16: 194/175/186/176
+//   gradients 128 x 128, 16 heads 325/398/598, 64: 1217/917/812, 96: 1800/1351/1450, 128: 2175/1790/1593
+inline double walk_cost(const GdrArgs& a, int TN) {
+  const bool two = a.dtype == 1 && a.K <= 64 && (TN == 1 || TN == 2);
+  const int columns = TN ? 16 * TN : 128;
+  const long long blocks = (long long)a.N * a.H * ((a.V + columns - 1) / columns);
+  const double chain = TN == 0 ? 165 : a.dtype == 1 && a.K <= 64 ? (TN == 1 ? 72 : TN == 2 ? 95 : 140) : (TN == 1 ? 80 : TN == 2 ? 105 : 160);
+  const double pair = two ? (TN == 1 ? 115 : 165) : 2 * chain;  // two blocks on one SM
+  if (a.packed) return std::max(chain, 0.5 * blocks / 148 * pair / 2);
+  const long long rounds = (blocks + 147) / 148;
+  return rounds / 2 * pair + rounds % 2 * chain;
+}
+
+// The tiles a block, by that cost (fp32 inputs: at most two; their second parts fill the registers).
+inline int tiles_a_block(const GdrArgs& a) {
+  int best = 1;
+  for (int TN = 2; TN <= (a.dtype == 1 ? 4 : 2); TN *= 2)
+    if (walk_cost(a, TN) < walk_cost(a, best)) best = TN;
+  return best;
 }
 
 template <typename T, int KP, int TN, bool GRAD>
@@ -450,7 +474,7 @@ cudaError_t launch_walk_tn(const GdrArgs& a, const char* keys, const char* recor
 
 template <typename T, int KP, bool GRAD>
 cudaError_t launch_walk(const GdrArgs& a, const char* keys, const char* records, const Kept& kept, cudaStream_t stream) {
-  const int tn = tiles_a_block<T>(a);
+  const int tn = tiles_a_block(a);
   if constexpr (sizeof(T) == 2)
     if (tn == 4) return launch_walk_tn<T, KP, 4, GRAD>(a, keys, records, kept, stream);
   return tn == 2 ? launch_walk_tn<T, KP, 2, GRAD>(a, keys, records, kept, stream)

@@ -179,7 +179,7 @@ def _load(path):
     L.mlstm_gdr_bwd_workspace_size.restype = Z
     L.mlstm_gdr_bwd.argtypes = [P] + [P] * 9 + [GdrStride] * 3 + [P] * 7 + [Z, P]
     L.mlstm_gdr_bwd.restype = I
-    L.mlstm_gdr_status.argtypes = [P, I, P, P]
+    L.mlstm_gdr_status.argtypes = [P, P, P]
     L.mlstm_gdr_status.restype = I
     L.mlstm_rms_norm.argtypes = [P] + [P] * 7
     L.mlstm_rms_norm.restype = I
@@ -668,10 +668,10 @@ def gdr_bwd_workspace_size(params: GdrParams) -> int:
     return int(lib().mlstm_gdr_bwd_workspace_size(ctypes.byref(params)))
 
 
-def gdr_status(params: GdrParams, workspace, *, backward: bool = False, stream=None) -> int:
-    """Outcome of the bounded waits of the last gdr_fwd (or gdr_bwd) with these params and this workspace
+def gdr_status(params: GdrParams, workspace, *, stream=None) -> int:
+    """Outcome of the bounded waits of the last gdr_fwd with these params and this workspace
     (mlstm_gdr_status; synchronises): 0 ok, 8 a wait ran out (MLSTM_ERR_TIMEOUT)."""
-    return int(lib().mlstm_gdr_status(ctypes.byref(params), int(backward), _ptr(workspace), _stream_ptr(stream)))
+    return int(lib().mlstm_gdr_status(ctypes.byref(params), _ptr(workspace), _stream_ptr(stream)))
 
 
 def _like(t, packed):
@@ -745,8 +745,7 @@ def gdr_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None):
     return _on(dev, stream, (q, k, v, g, beta, S, slots, o), body)
 
 
-def gdr_bwd(q, k, v, g, beta, do, S0=None, dS=None, *, seq_offsets=None, workspace=None, stream=None,
-            wait_limit_cycles: int = 0):
+def gdr_bwd(q, k, v, g, beta, do, S0=None, dS=None, *, seq_offsets=None, workspace=None, stream=None):
     """Gradients of the gated delta rule (mlstm_gdr_bwd): gdr_fwd's inputs, do [B,H,T,V] and dS
     [N,H,K,V] fp32 (the gradient of the final states) or None.  Returns a dict: dq, dk, dv in the inputs'
     type, laid out like them where they fill their memory; dg, dbeta [B,H,T] and dS0 [N,H,K,V] fp32.
@@ -758,8 +757,7 @@ def gdr_bwd(q, k, v, g, beta, do, S0=None, dS=None, *, seq_offsets=None, workspa
     _want("S0", S0, states, _F32, dev)
     _want("dS", dS, states, _F32, dev)
     packed = seq_offsets is not None
-    p = _gdr_pack(sizes, N if packed else 0, q.dtype, 0, _gdr_inputs(q, k, v, g, beta), _strides("do", do),
-                  wait_limit_cycles)
+    p = _gdr_pack(sizes, N if packed else 0, q.dtype, 0, _gdr_inputs(q, k, v, g, beta), _strides("do", do), 0)
 
     def body(cs):
         new = torch.zeros if packed else torch.empty

@@ -30,7 +30,7 @@ def fwd(p, S0=None, off=None, S_out=None, ws=None, ws_bytes=0, **kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(B=-1), SHAPE), (dict(T=-1), SHAPE), (dict(T=2**30 + 1), SHAPE), (dict(K=12), SHAPE), (dict(K=0), SHAPE),
+    (dict(B=65535, T=2**22), SHAPE), (dict(B=-1), SHAPE), (dict(T=-1), SHAPE), (dict(T=2**30 + 1), SHAPE), (dict(K=12), SHAPE), (dict(K=0), SHAPE),
     (dict(K=264), SHAPE), (dict(V=4), SHAPE), (dict(V=0), SHAPE), (dict(HK=3, H=4), SHAPE), (dict(HK=0, H=2), SHAPE),
     (dict(H=65536, HK=1), SHAPE), (dict(B=65536), SHAPE), (dict(dtype=2), DTYPE), (dict(mode=3), SHAPE),
     (dict(K=136, mode=2), SHAPE), (dict(num_seqs=2, B=2), SHAPE), (dict(num_seqs=-1), SHAPE),
@@ -124,12 +124,11 @@ def rms(rows=4, D=64, dtype=0, quant=0, group=0, eps=1e-6, **kw):
 
 def test_status_refusals():
     L = mlstm.lib()
-    many = gdr(B=4, HK=16, H=16, T=64, K=64, V=64, dtype=1, mode=2)
-    assert L.mlstm_gdr_status(None, 0, A[0], None) == NULL
-    assert L.mlstm_gdr_status(ctypes.byref(gdr(K=12)), 0, A[0], None) == SHAPE
-    assert L.mlstm_gdr_status(ctypes.byref(gdr(K=256)), 1, A[0], None) == SHAPE  # no gradients of this width
-    for backward in (0, 1):
-        assert L.mlstm_gdr_status(ctypes.byref(many), backward, None, None) == NULL  # its error word lives there
+    many = gdr(B=8, HK=16, H=16, T=64, K=64, V=128, dtype=1, mode=2)
+    assert L.mlstm_gdr_status(None, A[0], None) == NULL
+    assert L.mlstm_gdr_status(ctypes.byref(gdr(K=12)), A[0], None) == SHAPE
+    assert L.mlstm_gdr_status(ctypes.byref(gdr(dtype=3)), A[0], None) == DTYPE
+    assert L.mlstm_gdr_status(ctypes.byref(many), None, None) == NULL  # its error word lives there
 
 
 def test_rms_refusals():
