@@ -3,6 +3,7 @@
 // gdr_prep_kernel computes for all chunks at once what does not depend on the state: k and q in 16-bit
 // parts, R, P and the factors of each token.  gdr_walk_kernel then takes each sequence's chunks in order.
 #include "gdr_walk.cuh"
+#include "sm100.cuh"
 
 namespace mlstm {
 namespace gdr {
@@ -22,6 +23,7 @@ constexpr int prep_smem() {
 template <int STEPS>
 __device__ __forceinline__ void product_tf32(float (&c)[4], const float* A, const float* b, const float* B, int lane) {
   const int g = lane >> 2, q = lane & 3;
+  float hl[4] = {0.f, 0.f, 0.f, 0.f}, lh[4] = {0.f, 0.f, 0.f, 0.f};  // chains of their own
 #pragma unroll
   for (int k = 0; k < STEPS; ++k) {
     const int i = k * 8 + q;
@@ -33,29 +35,35 @@ __device__ __forceinline__ void product_tf32(float (&c)[4], const float* A, cons
     split_tf32(A[(g + 8) * kMs + i + 4] * b1, ah[3], al[3]);
     split_tf32(B[i * kMs + g], bh[0], bl[0]);
     split_tf32(B[(i + 4) * kMs + g], bh[1], bl[1]);
-    mma_tf32(c, al, bh);
-    mma_tf32(c, ah, bl);
+    mma_tf32(lh, al, bh);
+    mma_tf32(hl, ah, bl);
     mma_tf32(c, ah, bh);
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c[e] += hl[e] + lh[e];
 }
 
 // Joins the solved N x N diagonal blocks at `top` and top + N: with 1 the upper and 2 the lower block,
 //     X = M21 + M21 b1 R11,   R21 = -(X + R22 b2 X).
-// One warp a 16 x 8 tile (mt, nt); X has N rows of its own.  A barrier lies between the two halves.
-template <int N>
-__device__ __forceinline__ void join_half(bool second, const float* M, float* R, float* X, const float* beta, int top,
-                                          int mt, int nt, int lane) {
+// One warp a 16 x 8 tile (mt, nt); X has N rows of its own, and `meet` waits for the warps of the same nt.
+template <int N, typename Meet>
+__device__ __forceinline__ void join(const float* M, float* R, float* X, const float* beta, int top, int mt, int nt, int lane,
+                                     Meet meet) {
   const int low = top + N, r = mt * 16 + (lane >> 2), cc = nt * 8 + 2 * (lane & 3);
-  const float* from = second ? X : M + low * kMs + top;
-  float c[4] = {from[r * kMs + cc], from[r * kMs + cc + 1], from[(r + 8) * kMs + cc], from[(r + 8) * kMs + cc + 1]};
-  if (second)
-    product_tf32<N / 8>(c, R + (low + mt * 16) * kMs + low, beta + low, X + nt * 8, lane);
-  else
-    product_tf32<N / 8>(c, M + (low + mt * 16) * kMs + top, beta + top, R + top * kMs + top + nt * 8, lane);
-  float* to = second ? R + low * kMs + top : X;
-  const float sign = second ? -1.f : 1.f;
-  to[r * kMs + cc] = sign * c[0], to[r * kMs + cc + 1] = sign * c[1];
-  to[(r + 8) * kMs + cc] = sign * c[2], to[(r + 8) * kMs + cc + 1] = sign * c[3];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const float* from = half ? X : M + low * kMs + top;
+    float c[4] = {from[r * kMs + cc], from[r * kMs + cc + 1], from[(r + 8) * kMs + cc], from[(r + 8) * kMs + cc + 1]};
+    if (half)
+      product_tf32<N / 8>(c, R + (low + mt * 16) * kMs + low, beta + low, X + nt * 8, lane);
+    else
+      product_tf32<N / 8>(c, M + (low + mt * 16) * kMs + top, beta + top, R + top * kMs + top + nt * 8, lane);
+    float* to = half ? R + low * kMs + top : X;
+    const float sign = half ? -1.f : 1.f;
+    to[r * kMs + cc] = sign * c[0], to[r * kMs + cc + 1] = sign * c[1];
+    to[(r + 8) * kMs + cc] = sign * c[2], to[(r + 8) * kMs + cc + 1] = sign * c[3];
+    if (!half) meet();
+  }
 }
 
 // One block for each chunk and key head; the value heads that share it follow one another.  The two
@@ -83,6 +91,19 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
   {  // k, q: four threads a row
     const int row = tid >> 2, part = tid & 3;
     char* out = keys + (rec * a.HK + hk) * keys_bytes(KP, NP);
+    uint4 bits[2][KP / 32];  // (16-bit inputs: all loads before the first use)
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      if constexpr (NP == 1) {
+        const GdrStride st = which ? a.sq : a.sk;
+        const T* src = (const T*)(which ? a.q : a.k) + sq_.b * st.b + hk * st.h + (t0 + row) * st.t;
+#pragma unroll
+        for (int j = 0; j < KP / 32; ++j) {
+          const int col = (j * 4 + part) * 8;
+          bits[which][j] = row < len && col < a.K ? *reinterpret_cast<const uint4*>(src + col) : make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const GdrStride st = which ? a.sq : a.sk;
@@ -91,7 +112,16 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
 #pragma unroll
       for (int j = 0; j < KP / 32; ++j) {
         const int col = (j * 4 + part) * 8;
-        load8<T>(src + col, row < len && col < a.K, x[j]);
+        if constexpr (NP == 1) {
+          const uint32_t u[4] = {bits[which][j].x, bits[which][j].y, bits[which][j].z, bits[which][j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack_bf16(u[e]);
+            x[j][2 * e] = f.x, x[j][2 * e + 1] = f.y;
+          }
+        } else {
+          load8<T>(src + col, row < len && col < a.K, x[j]);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[j][e]));
       }
@@ -117,7 +147,26 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
   }
   __syncthreads();
 
-  // k k^T and q k^T: a warp has 16 rows and 32 columns
+  auto gates = [&](int h) {  // cumulative log decays, two tokens a lane, in 64 bits
+    const float* g = a.g + sq_.b * a.sg.b + h * a.sg.h;
+    const float* be = a.beta + sq_.b * a.sb.b + h * a.sb.h;
+    const int t = 2 * lane;
+    const double2 sum = cumulative(g, a.sg.t, t0, len, lane);
+    const double last = __shfl_sync(0xffffffffu, sum.y, 31);
+    const float2 g0 = two_parts(sum.x), g1 = two_parts(sum.y);
+    G[t] = g0, G[t + 1] = g1;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const double x = e ? sum.y : sum.x;
+      const float gam = expf((float)x), w = expf((float)(last - x));
+      fac[kGam * kL + t + e] = gam, fac[kW * kL + t + e] = w;
+      fac[kGK * kL + t + e] = gam * fac[kKInv * kL + t + e], fac[kGQ * kL + t + e] = gam * fac[kQInv * kL + t + e];
+      fac[kWK * kL + t + e] = w * fac[kKInv * kL + t + e];
+      fac[kBeta * kL + t + e] = t + e < len ? be[(t0 + t + e) * a.sb.t] : 0.f;
+    }
+  };
+
+  // k k^T and q k^T: a warp has 16 rows and 32 columns; one that has none below the diagonal takes the gates
   const int r0 = (warp & 3) * 16, c0 = (warp >> 2) * 32;
   const bool lower = c0 <= r0 + 15;
   float kk_[4][4], qk[4][4];
@@ -161,29 +210,14 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
         kk_[j][e] = kk_[j][e] * fac[kKInv * kL + t] * fac[kKInv * kL + s];
         qk[j][e] = qk[j][e] * fac[kQInv * kL + t] * fac[kKInv * kL + s];
       }
+  } else if (warp == 4) {
+    gates(hk * (a.H / a.HK));
   }
+  __syncthreads();
 
   for (int h = hk * (a.H / a.HK); h < (hk + 1) * (a.H / a.HK); ++h) {
     char* out = records + (rec * a.H + h) * record_bytes(P2);
-    if (warp == 0) {  // cumulative log decays, two tokens a lane, in 64 bits
-      const float* g = a.g + sq_.b * a.sg.b + h * a.sg.h;
-      const float* be = a.beta + sq_.b * a.sb.b + h * a.sb.h;
-      const int t = 2 * lane;
-      const double2 sum = cumulative(g, a.sg.t, t0, len, lane);
-      const double last = __shfl_sync(0xffffffffu, sum.y, 31);
-      const float2 g0 = two_parts(sum.x), g1 = two_parts(sum.y);
-      G[t] = g0, G[t + 1] = g1;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const double x = e ? sum.y : sum.x;
-        const float gam = expf((float)x), w = expf((float)(last - x));
-        fac[kGam * kL + t + e] = gam, fac[kW * kL + t + e] = w;
-        fac[kGK * kL + t + e] = gam * fac[kKInv * kL + t + e], fac[kGQ * kL + t + e] = gam * fac[kQInv * kL + t + e];
-        fac[kWK * kL + t + e] = w * fac[kKInv * kL + t + e];
-        fac[kBeta * kL + t + e] = t + e < len ? be[(t0 + t + e) * a.sb.t] : 0.f;
-      }
-    }
-    __syncthreads();
+    float* fout = reinterpret_cast<float*>(out + (P2 ? 4 : 3) * kTile);
     // P, rows scaled, and M, of which blocks above the diagonal are never read
     float p[4][4], big[2] = {0.f, 0.f};
     zero(p);
@@ -233,7 +267,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
     for (int i = 0; i < 2; ++i) {
       const int t = r0 + (lane >> 2) + i * 8;
       const Scale sc = scale_of(fmaxf(pmax[t], pmax[kL + t]));
-      if (c0 == 0 && (lane & 3) == 0) fac[kPInv * kL + t] = sc.inv;
+      if (c0 == 0 && (lane & 3) == 0) fout[kPInv * kL + t] = sc.inv;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t hi, lo;
@@ -243,17 +277,17 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
         if constexpr (P2) *reinterpret_cast<uint32_t*>(at + kTile) = lo;
       }
     }
+    if (warp >= 4) {  // (the two warps of a pair of blocks; the other warps have nothing of R yet)
+      const int pair = (warp - 4) >> 1;
+      sm100::named_bar(1 + pair, 64);
+      join<16>(M, R, X + pair * 16 * kMs, beta, pair * 32, 0, warp & 1, lane, [] { __syncwarp(); });
+    } else {  // the factors but R's
+      for (int e = tid; e < kFactors * kL; e += 128)
+        if (e / kL != kRInv && e / kL != kPInv) fout[e] = fac[e];
+    }
     __syncthreads();
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (warp < 4) join_half<16>(half, M, R, X + (warp >> 1) * 16 * kMs, beta, (warp >> 1) * 32, 0, warp & 1, lane);
-      __syncthreads();
-    }
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      join_half<32>(half, M, R, X, beta, 0, warp >> 2, warp & 3, lane);
-      __syncthreads();
-    }
+    join<32>(M, R, X, beta, 0, warp >> 2, warp & 3, lane, [&] { sm100::named_bar(3 + (warp & 3), 64); });
+    __syncthreads();
     {  // R, rows scaled: four threads a row, 16 columns each, zeros above the diagonal's block
       const int row = tid >> 2, part = tid & 3;
       const bool below = part * 16 <= row;
@@ -268,7 +302,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const Scale sc = scale_of(m);
-      if (part == 0) fac[kRInv * kL + row] = sc.inv;
+      if (part == 0) fout[kRInv * kL + row] = sc.inv;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t hi[4], lo[4];
@@ -279,10 +313,11 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
         *reinterpret_cast<uint4*>(out + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
-    __syncthreads();
-    float* fout = reinterpret_cast<float*>(out + (P2 ? 4 : 3) * kTile);
-    for (int e = tid; e < kFactors * kL; e += kPrepThreads) fout[e] = fac[e];
-    __syncthreads();  // fac, M, R belong to the next head
+    if (h + 1 < (hk + 1) * (a.H / a.HK)) {  // fac, M, R belong to the next head
+      __syncthreads();
+      if (warp == 4) gates(h + 1);
+      __syncthreads();
+    }
   }
 }
 
