@@ -92,6 +92,15 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
       if (c > 0) fetch_chunk<T, KP, TN, true>(a, s, rec - 1, h, c - 1, col0, keys, records, smem_u32(slot(c - 1)));
       cp_commit();
     }
+    if (live && c > 0) {  // on its way to L2 for the chunk before: a quarter of the state and of Z' there
+      const char* state_at = kept.S + ((((size_t)(rec + n)) * a.H + h) * tiles + tile) * 2 * 16 * KP * 2;
+      const char* z_at = (const char*)(kept.Z + (base - (size_t)a.H * tiles) * 16 * kL);
+      constexpr int lines = 2 * 16 * KP * 2 / 128 / kQuarter;
+      if (lane < lines)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(state_at + (w * lines + lane) * 128));
+      else if (lane < lines + 8)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(z_at + (w * 8 + lane - lines) * 128));
+    }
     // this quarter's share of dO by P's scale, and gam dO
     float x[2][4], y[2][4];
     {

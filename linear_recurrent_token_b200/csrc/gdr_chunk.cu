@@ -19,13 +19,15 @@ constexpr int prep_smem() {
 }
 
 // c += (A diag(b)) B for a 16 x 8 tile of c, k = 8 STEPS: fp32 matrices in shared memory (pitch kMs) as two
-// tf32 parts each, whose exponent is fp32's: no scaling.
+// tf32 parts each, whose exponent is fp32's: no scaling.  Only steps from .. upto - 1 hold anything.
 template <int STEPS>
-__device__ __forceinline__ void product_tf32(float (&c)[4], const float* A, const float* b, const float* B, int lane) {
+__device__ __forceinline__ void product_tf32(float (&c)[4], const float* A, const float* b, const float* B, int from, int upto,
+                                             int lane) {
   const int g = lane >> 2, q = lane & 3;
-  float hl[4] = {0.f, 0.f, 0.f, 0.f}, lh[4] = {0.f, 0.f, 0.f, 0.f};  // chains of their own
+  float hl[4] = {0.f, 0.f, 0.f, 0.f}, lh[4] = {0.f, 0.f, 0.f, 0.f};  // sums of their own: shorter chains
 #pragma unroll
   for (int k = 0; k < STEPS; ++k) {
+    if (k < from || k >= upto) continue;
     const int i = k * 8 + q;
     const float b0 = b[i], b1 = b[i + 4];
     uint32_t ah[4], al[4], bh[2], bl[2];
@@ -55,9 +57,9 @@ __device__ __forceinline__ void join(const float* M, float* R, float* X, const f
     const float* from = half ? X : M + low * kMs + top;
     float c[4] = {from[r * kMs + cc], from[r * kMs + cc + 1], from[(r + 8) * kMs + cc], from[(r + 8) * kMs + cc + 1]};
     if (half)
-      product_tf32<N / 8>(c, R + (low + mt * 16) * kMs + low, beta + low, X + nt * 8, lane);
+      product_tf32<N / 8>(c, R + (low + mt * 16) * kMs + low, beta + low, X + nt * 8, 0, 2 * (mt + 1), lane);
     else
-      product_tf32<N / 8>(c, M + (low + mt * 16) * kMs + top, beta + top, R + top * kMs + top + nt * 8, lane);
+      product_tf32<N / 8>(c, M + (low + mt * 16) * kMs + top, beta + top, R + top * kMs + top + nt * 8, nt, N / 8, lane);
     float* to = half ? R + low * kMs + top : X;
     const float sign = half ? -1.f : 1.f;
     to[r * kMs + cc] = sign * c[0], to[r * kMs + cc + 1] = sign * c[1];
@@ -87,6 +89,35 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
   const int hk = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long rec = blockIdx.x, t0 = sq_.lo + (long long)c * kL;
   const int len = (int)min((long long)kL, sq_.len - (long long)c * kL);
+
+  // A head's gates, two tokens a lane of warp 4: what it reads, well ahead, and their sums, in 64 bits.
+  float gate[2], write[2];
+  auto load_gates = [&](int h) {
+    const float* g = a.g + sq_.b * a.sg.b + h * a.sg.h;
+    const float* be = a.beta + sq_.b * a.sb.b + h * a.sb.h;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int t = 2 * lane + e;
+      gate[e] = t < len ? g[(t0 + t) * a.sg.t] : 0.f;
+      write[e] = t < len ? be[(t0 + t) * a.sb.t] : 0.f;
+    }
+  };
+  auto gates = [&] {
+    const int t = 2 * lane;
+    const double2 sum = cumulative(gate[0], gate[1], lane);
+    const double last = __shfl_sync(0xffffffffu, sum.y, 31);
+    G[t] = two_parts(sum.x * kPerLn2), G[t + 1] = two_parts(sum.y * kPerLn2);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const double x = e ? sum.y : sum.x;
+      const float gam = expf((float)x), w = expf((float)(last - x));
+      fac[kGam * kL + t + e] = gam, fac[kW * kL + t + e] = w;
+      fac[kGK * kL + t + e] = gam * fac[kKInv * kL + t + e], fac[kGQ * kL + t + e] = gam * fac[kQInv * kL + t + e];
+      fac[kWK * kL + t + e] = w * fac[kKInv * kL + t + e];
+      fac[kBeta * kL + t + e] = write[e];
+    }
+  };
+  if (warp == 4) load_gates(hk * (a.H / a.HK));
 
   {  // k, q: four threads a row
     const int row = tid >> 2, part = tid & 3;
@@ -147,34 +178,15 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
   }
   __syncthreads();
 
-  auto gates = [&](int h) {  // cumulative log decays, two tokens a lane, in 64 bits
-    const float* g = a.g + sq_.b * a.sg.b + h * a.sg.h;
-    const float* be = a.beta + sq_.b * a.sb.b + h * a.sb.h;
-    const int t = 2 * lane;
-    const double2 sum = cumulative(g, a.sg.t, t0, len, lane);
-    const double last = __shfl_sync(0xffffffffu, sum.y, 31);
-    const float2 g0 = two_parts(sum.x), g1 = two_parts(sum.y);
-    G[t] = g0, G[t + 1] = g1;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const double x = e ? sum.y : sum.x;
-      const float gam = expf((float)x), w = expf((float)(last - x));
-      fac[kGam * kL + t + e] = gam, fac[kW * kL + t + e] = w;
-      fac[kGK * kL + t + e] = gam * fac[kKInv * kL + t + e], fac[kGQ * kL + t + e] = gam * fac[kQInv * kL + t + e];
-      fac[kWK * kL + t + e] = w * fac[kKInv * kL + t + e];
-      fac[kBeta * kL + t + e] = t + e < len ? be[(t0 + t + e) * a.sb.t] : 0.f;
-    }
-  };
-
   // k k^T and q k^T: a warp has 16 rows and 32 columns; one that has none below the diagonal takes the gates
   const int r0 = (warp & 3) * 16, c0 = (warp >> 2) * 32;
-  const bool lower = c0 <= r0 + 15;
+  const bool upper = warp == 4 || warp == 5;  // its products lie above the diagonal
   float kk_[4][4], qk[4][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) kk_[j][e] = qk[j][e] = 0.f;
-  if (lower) {
+  if (!upper) {
 #pragma unroll
     for (int s = 0; s < KP / 16; ++s) {
       const int at = piece_at<KP>(r0 + bt_row(lane), s * 16 + bt_col(lane));  // an A operand's rows
@@ -211,7 +223,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
         qk[j][e] = qk[j][e] * fac[kQInv * kL + t] * fac[kKInv * kL + s];
       }
   } else if (warp == 4) {
-    gates(hk * (a.H / a.HK));
+    gates();
   }
   __syncthreads();
 
@@ -221,7 +233,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
     // P, rows scaled, and M, of which blocks above the diagonal are never read
     float p[4][4], big[2] = {0.f, 0.f};
     zero(p);
-    if (lower) {
+    if (!upper) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -241,8 +253,9 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
     }
     __syncthreads();
     const float* beta = fac + kBeta * kL;
-    if (lane < 16 && warp >= 4) {  // R: a 16 x 16 diagonal block a warp, a column a lane
-      const int top = (warp - 4) * 16, s = lane;
+    if (upper) {  // R: two 16 x 16 diagonal blocks a warp, a column a lane, then their join
+      if (warp == 4 && h + 1 < (hk + 1) * (a.H / a.HK)) load_gates(h + 1);
+      const int pair = warp - 4, top = pair * 32 + (lane & 16), s = lane & 15;
       float y[16];  // beta_i R[i][s]
 #pragma unroll
       for (int t = 0; t < 16; ++t) {
@@ -257,32 +270,27 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
         const float r = t > s ? -(M[(top + t) * kMs + top + s] + ((x[0] + x[1]) + (x[2] + x[3]))) : 0.f;
         R[(top + t) * kMs + top + s] = r;
         y[t] = beta[top + t] * r;
+        if (lane >= 16) R[(pair * 32 + t) * kMs + pair * 32 + lane] = 0.f;  // the second join reads these too
       }
-    } else if (warp == 4 || warp == 6) {  // the blocks above the diagonal that the second join reads
-      const int top = (warp - 4) * 16;
+      __syncwarp();
+      join<16>(M, R, X + pair * 16 * kMs, beta, pair * 32, 0, 0, lane, [] { __syncwarp(); });
+      join<16>(M, R, X + pair * 16 * kMs, beta, pair * 32, 0, 1, lane, [] { __syncwarp(); });
+    } else {  // P, and the factors but R's
 #pragma unroll
-      for (int t = 0; t < 16; ++t) R[(top + t) * kMs + top + lane] = 0.f;
-    }
+      for (int i = 0; i < 2; ++i) {
+        const int t = r0 + (lane >> 2) + i * 8;
+        const Scale sc = scale_of(fmaxf(pmax[t], pmax[kL + t]));
+        if (c0 == 0 && (lane & 3) == 0) fout[kPInv * kL + t] = sc.inv;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = r0 + (lane >> 2) + i * 8;
-      const Scale sc = scale_of(fmaxf(pmax[t], pmax[kL + t]));
-      if (c0 == 0 && (lane & 3) == 0) fout[kPInv * kL + t] = sc.inv;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t hi, lo;
-        split(p[j][2 * i] * sc.mul, p[j][2 * i + 1] * sc.mul, hi, lo);
-        char* at = out + 2 * kTile + piece_at<kL>(t, c0 + j * 8) + (lane & 3) * 4;
-        *reinterpret_cast<uint32_t*>(at) = hi;
-        if constexpr (P2) *reinterpret_cast<uint32_t*>(at + kTile) = lo;
+        for (int j = 0; j < 4; ++j) {
+          uint32_t hi, lo;
+          split(p[j][2 * i] * sc.mul, p[j][2 * i + 1] * sc.mul, hi, lo);
+          char* at = out + 2 * kTile + piece_at<kL>(t, c0 + j * 8) + (lane & 3) * 4;
+          *reinterpret_cast<uint32_t*>(at) = hi;
+          if constexpr (P2) *reinterpret_cast<uint32_t*>(at + kTile) = lo;
+        }
       }
-    }
-    if (warp >= 4) {  // (the two warps of a pair of blocks; the other warps have nothing of R yet)
-      const int pair = (warp - 4) >> 1;
-      sm100::named_bar(1 + pair, 64);
-      join<16>(M, R, X + pair * 16 * kMs, beta, pair * 32, 0, warp & 1, lane, [] { __syncwarp(); });
-    } else {  // the factors but R's
-      for (int e = tid; e < kFactors * kL; e += 128)
+      for (int e = warp < 4 ? tid : tid - 64; e < kFactors * kL; e += 192)
         if (e / kL != kRInv && e / kL != kPInv) fout[e] = fac[e];
     }
     __syncthreads();
@@ -311,11 +319,15 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
         const int at = piece_at<kL>(row, part * 16 + i * 8);
         *reinterpret_cast<uint4*>(out + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(out + kTile + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (row < 32 && part >= 2) {  // P's upper quarter
+          *reinterpret_cast<uint4*>(out + 2 * kTile + at) = make_uint4(0, 0, 0, 0);
+          if constexpr (P2) *reinterpret_cast<uint4*>(out + 3 * kTile + at) = make_uint4(0, 0, 0, 0);
+        }
       }
     }
     if (h + 1 < (hk + 1) * (a.H / a.HK)) {  // fac, M, R belong to the next head
       __syncthreads();
-      if (warp == 4) gates(h + 1);
+      if (warp == 4) gates();
       __syncthreads();
     }
   }

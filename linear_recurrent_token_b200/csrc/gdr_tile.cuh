@@ -46,7 +46,7 @@ constexpr int kQuarter = 4;  // warps of a tile of 16 value columns
 // [64][64] fp16, then the per-token factors.  The 16-byte pieces of a row of these tiles are permuted
 // by the row, so that a record is copied as it is and ldmatrix meets no bank conflicts.
 // kGK = gam / k's scale and so on: what the passes over the chunks multiply by; the rest is for the others.
-enum { kGK = 0, kGQ, kWK, kBeta, kRInv, kPInv, kGam, kW, kKInv, kQInv, kG, kFactors = kG + 2 };  // kG: G in two parts
+enum { kGK = 0, kGQ, kWK, kBeta, kRInv, kPInv, kGam, kW, kKInv, kQInv, kG, kFactors = kG + 2 };  // kG: G / ln 2 in two parts
 constexpr int kTile = kL * kL * 2;
 constexpr int kFactorBytes = kFactors * kL * 4;
 __host__ __device__ constexpr int keys_bytes(int KP, int np) { return 2 * np * kL * KP * 2; }
@@ -110,19 +110,19 @@ __device__ __forceinline__ bool find_chunk(const GdrArgs& a, long long rec, int*
 // 64 such terms keep every smaller one exactly in 64 bits.  NaN stays NaN.
 __device__ __forceinline__ double log_decay(float g) { return g < -1e4f ? -1e4 : (double)g; }
 
-// A sum in 64 bits as two fp32 parts, and the decay e^(a - b) between two of them: the difference keeps
+// A sum in 64 bits (in units of ln 2) as two fp32 parts, and the decay 2^(a - b) between two: the difference keeps
 // fp32's relative accuracy however large the sums are.
+constexpr double kPerLn2 = 1.4426950408889634;
 __device__ __forceinline__ float2 two_parts(double x) {
   const float hi = (float)x;
   return make_float2(hi, (float)(x - hi));
 }
-__device__ __forceinline__ float decay_between(float2 a, float2 b) { return expf((a.x - b.x) + (a.y - b.y)); }
+__device__ __forceinline__ float decay_between(float2 a, float2 b) { return exp2f((a.x - b.x) + (a.y - b.y)); }
 
-// Cumulative log decays of the chunk that begins at token t0: lane has those of tokens 2 lane (x) and
-// 2 lane + 1 (y); no decay from `len` on.
-__device__ __forceinline__ double2 cumulative(const float* g, long long st, long long t0, int len, int lane) {
-  const int t = 2 * lane;
-  const double x0 = t < len ? log_decay(g[(t0 + t) * st]) : 0.0, x1 = t + 1 < len ? log_decay(g[(t0 + t + 1) * st]) : 0.0;
+// Cumulative log decays of a chunk: lane has those of tokens 2 lane (x) and 2 lane + 1 (y), and brings theirs
+// (0 where there is no token).
+__device__ __forceinline__ double2 cumulative(float g0, float g1, int lane) {
+  const double x0 = log_decay(g0), x1 = log_decay(g1);
   double sum = x0 + x1;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
