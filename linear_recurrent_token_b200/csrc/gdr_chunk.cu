@@ -18,6 +18,14 @@ constexpr int prep_smem() {
   return (keys_bytes(KP, NP) > matrices ? keys_bytes(KP, NP) : matrices) + kFactorBytes + 2 * kL * 4;
 }
 
+__device__ __forceinline__ float2 times2(float2 x, float f) {
+  float2 y;
+  asm("{.reg .b64 p, q, r;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %4};\n mul.rn.f32x2 r, p, q;\n mov.b64 {%0, %1}, r;}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(x.x), "f"(x.y), "f"(f));
+  return y;
+}
+
 // c += (A diag(b)) B for a 16 x 8 tile of c, k = 8 STEPS: fp32 matrices in shared memory (pitch kMs) as two
 // tf32 parts each, whose exponent is fp32's: no scaling.  Only steps from .. upto - 1 hold anything.
 template <int STEPS>
@@ -71,8 +79,8 @@ __device__ __forceinline__ void join(const float* M, float* R, float* X, const f
 // One block for each chunk and key head; the value heads that share it follow one another.  The two
 // 64 x 64 x KP products run on the tensor cores; of the triangular solve, four 16 x 16 diagonal blocks go
 // row by row in fp32 and two rounds of joins on the tensor cores again.
-template <typename T, int KP, bool P2>
-__global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs a, char* keys, char* records) {
+template <typename T, int KP, bool P2, bool ONE>
+__global__ void __launch_bounds__(kPrepThreads, ONE && sizeof(T) == 2 ? 4 : 3) gdr_prep_kernel(const GdrArgs a, char* keys, char* records) {
   constexpr int NP = sizeof(T) == 4 ? 2 : 1;
   extern __shared__ __align__(16) char smem[];
   char* sk = smem;  // k parts, then q parts
@@ -86,7 +94,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
   int n, c;
   Seq sq_;
   if (!find_chunk(a, blockIdx.x, &n, &sq_, &c)) return;
-  const int hk = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int hk = blockIdx.y, group = ONE ? 1 : a.H / a.HK, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long rec = blockIdx.x, t0 = sq_.lo + (long long)c * kL;
   const int len = (int)min((long long)kL, sq_.len - (long long)c * kL);
 
@@ -117,61 +125,78 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
       fac[kBeta * kL + t + e] = write[e];
     }
   };
-  if (warp == 4) load_gates(hk * (a.H / a.HK));
+  if (warp == 4) load_gates(hk * group);
 
   {  // k, q: four threads a row
     const int row = tid >> 2, part = tid & 3;
     char* out = keys + (rec * a.HK + hk) * keys_bytes(KP, NP);
-    uint4 bits[2][KP / 32];  // (16-bit inputs: all loads before the first use)
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      if constexpr (NP == 1) {
-        const GdrStride st = which ? a.sq : a.sk;
-        const T* src = (const T*)(which ? a.q : a.k) + sq_.b * st.b + hk * st.h + (t0 + row) * st.t;
-#pragma unroll
-        for (int j = 0; j < KP / 32; ++j) {
-          const int col = (j * 4 + part) * 8;
-          bits[which][j] = row < len && col < a.K ? *reinterpret_cast<const uint4*>(src + col) : make_uint4(0, 0, 0, 0);
-        }
-      }
-    }
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
+    auto source = [&](int which) {
       const GdrStride st = which ? a.sq : a.sk;
-      const T* src = (const T*)(which ? a.q : a.k) + sq_.b * st.b + hk * st.h + (t0 + row) * st.t;
-      float x[KP / 32][8], m = 0.f;
-#pragma unroll
-      for (int j = 0; j < KP / 32; ++j) {
-        const int col = (j * 4 + part) * 8;
-        if constexpr (NP == 1) {
-          const uint32_t u[4] = {bits[which][j].x, bits[which][j].y, bits[which][j].z, bits[which][j].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack_bf16(u[e]);
-            x[j][2 * e] = f.x, x[j][2 * e + 1] = f.y;
-          }
-        } else {
-          load8<T>(src + col, row < len && col < a.K, x[j]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[j][e]));
-      }
+      return (const T*)(which ? a.q : a.k) + sq_.b * st.b + hk * st.h + (t0 + row) * st.t;
+    };
+    auto scale_row = [&](int which, float m) {
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const Scale sc = scale_of(m);
       if (part == 0) fac[(which ? kQInv : kKInv) * kL + row] = sc.inv;
+      return sc.mul;
+    };
+    auto put = [&](int which, int j, int plane, const uint32_t (&w)[4]) {
+      const int at = (which ? keys_bytes(KP, NP) / 2 : 0) + plane * kL * KP * 2 + piece_at<KP>(row, (j * 4 + part) * 8);
+      const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(smem + at) = v;
+      *reinterpret_cast<uint4*>(out + at) = v;
+    };
+    if constexpr (NP == 1) {  // one part; all loads before the first use, magnitudes compared as integers
+      uint4 bits[2][KP / 32];
 #pragma unroll
-      for (int j = 0; j < KP / 32; ++j) {
-        uint32_t hi[4], lo[4];
+      for (int which = 0; which < 2; ++which)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split(x[j][2 * e] * sc.mul, x[j][2 * e + 1] * sc.mul, hi[e], lo[e]);
-        const int at = (which ? keys_bytes(KP, NP) / 2 : 0) + piece_at<KP>(row, (j * 4 + part) * 8);
-        const uint4 h4 = make_uint4(hi[0], hi[1], hi[2], hi[3]), l4 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<uint4*>(smem + at) = h4;
-        *reinterpret_cast<uint4*>(out + at) = h4;
-        if constexpr (NP == 2) {
-          *reinterpret_cast<uint4*>(smem + at + kL * KP * 2) = l4;
-          *reinterpret_cast<uint4*>(out + at + kL * KP * 2) = l4;
+        for (int j = 0; j < KP / 32; ++j) {
+          const int col = (j * 4 + part) * 8;
+          bits[which][j] = row < len && col < a.K ? *reinterpret_cast<const uint4*>(source(which) + col) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int j = 0; j < KP / 32; ++j) {
+          const uint4 u = bits[which][j];
+          m2 = __vmaxu2(__vmaxu2(m2, __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu)),
+                        __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+        }
+        const float mul = scale_row(which, __uint_as_float(max(m2 & 0xffff0000u, m2 << 16)));
+#pragma unroll
+        for (int j = 0; j < KP / 32; ++j) {
+          const uint32_t u[4] = {bits[which][j].x, bits[which][j].y, bits[which][j].z, bits[which][j].w};
+          uint32_t hi[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = times2(unpack_bf16(u[e]), mul);
+            hi[e] = pack(f.x, f.y);
+          }
+          put(which, j, 0, hi);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        float x[KP / 32][8], m = 0.f;
+#pragma unroll
+        for (int j = 0; j < KP / 32; ++j) {
+          const int col = (j * 4 + part) * 8;
+          load8<T>(source(which) + col, row < len && col < a.K, x[j]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[j][e]));
+        }
+        const float mul = scale_row(which, m);
+#pragma unroll
+        for (int j = 0; j < KP / 32; ++j) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split(x[j][2 * e] * mul, x[j][2 * e + 1] * mul, hi[e], lo[e]);
+          put(which, j, 0, hi);
+          put(which, j, 1, lo);
         }
       }
     }
@@ -227,23 +252,34 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
   }
   __syncthreads();
 
-  for (int h = hk * (a.H / a.HK); h < (hk + 1) * (a.H / a.HK); ++h) {
+  for (int h = hk * group; h < (hk + 1) * group; ++h) {
     char* out = records + (rec * a.H + h) * record_bytes(P2);
     float* fout = reinterpret_cast<float*>(out + (P2 ? 4 : 3) * kTile);
     // P, rows scaled, and M, of which blocks above the diagonal are never read
     float p[4][4], big[2] = {0.f, 0.f};
     zero(p);
     if (!upper) {
+      const int t = r0 + (lane >> 2);
+      const float2 Gt[2] = {G[t], G[t + 8]};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j) {
+        const int cj = c0 + j * 8, s = cj + (lane & 3) * 2;
+        if (cj > r0 + 15) continue;
+        const float4 Gs = *reinterpret_cast<const float4*>(G + s);
+        float mm[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int t = r0 + (lane >> 2) + (e >> 1) * 8, s = c0 + j * 8 + (lane & 3) * 2 + (e & 1);
-          const float D = s <= t ? decay_between(G[t], G[s]) : 0.f;
-          p[j][e] = s <= t ? qk[j][e] * D : 0.f;
+          const float D = decay_between(Gt[e >> 1], e & 1 ? make_float2(Gs.z, Gs.w) : make_float2(Gs.x, Gs.y));
+          p[j][e] = qk[j][e] * D, mm[e] = kk_[j][e] * D;
+          if (cj + 7 >= r0) {  // (a tile on the diagonal; decays that run backward may be infinite)
+            const int back = s + (e & 1) - t - (e >> 1) * 8;
+            p[j][e] = back <= 0 ? p[j][e] : 0.f, mm[e] = back < 0 ? mm[e] : 0.f;
+          }
           big[e >> 1] = fmaxf(big[e >> 1], fabsf(p[j][e]));
-          M[t * kMs + s] = s < t ? kk_[j][e] * D : 0.f;
         }
+        *reinterpret_cast<float2*>(M + t * kMs + s) = make_float2(mm[0], mm[1]);
+        *reinterpret_cast<float2*>(M + (t + 8) * kMs + s) = make_float2(mm[2], mm[3]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -254,7 +290,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
     __syncthreads();
     const float* beta = fac + kBeta * kL;
     if (upper) {  // R: two 16 x 16 diagonal blocks a warp, a column a lane, then their join
-      if (warp == 4 && h + 1 < (hk + 1) * (a.H / a.HK)) load_gates(h + 1);
+      if (warp == 4 && !ONE && h + 1 < (hk + 1) * group) load_gates(h + 1);
       const int pair = warp - 4, top = pair * 32 + (lane & 16), s = lane & 15;
       float y[16];  // beta_i R[i][s]
 #pragma unroll
@@ -325,7 +361,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
         }
       }
     }
-    if (h + 1 < (hk + 1) * (a.H / a.HK)) {  // fac, M, R belong to the next head
+    if (!ONE && h + 1 < (hk + 1) * group) {  // fac, M, R belong to the next head
       __syncthreads();
       if (warp == 4) gates();
       __syncthreads();
@@ -338,7 +374,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdr_prep_kernel(const GdrArgs
 template <typename T, int KP, bool P2>
 cudaError_t launch_prep(const GdrArgs& a, char* keys, char* records, cudaStream_t stream) {
   constexpr int smem = prep_smem<KP, sizeof(T) == 4 ? 2 : 1>();
-  const auto kernel = gdr_prep_kernel<T, KP, P2>;
+  const auto kernel = a.H == a.HK ? gdr_prep_kernel<T, KP, P2, true> : gdr_prep_kernel<T, KP, P2, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kernel<<<dim3((unsigned)record_count(a), a.HK), kPrepThreads, smem, stream>>>(a, keys, records);
