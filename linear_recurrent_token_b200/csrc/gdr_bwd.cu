@@ -15,10 +15,10 @@ namespace {
 
 // A block takes 16 TN value columns of one value head of one sequence, chunks from the last to the first.
 template <typename T, int KP, int TN>
-__global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrArgs a, const char* keys,
+__global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_back_kernel(const GdrArgs a, const char* keys,
                                                                       const char* records, const Kept kept) {
   using L = Stage<T, KP, TN, true>;
-  constexpr int NP = L::NP, NK = kept_parts<T>(), KS = KP / 64, threads = 32 * kQuarter * TN;
+  constexpr int NP = L::NP, NK = kept_parts<T>(), KS = KP / 64;
   // In exchange: dS, then beta dU in its place; dO by P's scale; gam dV; gam dO.
   constexpr int fy = L::fs;
   extern __shared__ __align__(128) char smem[];
@@ -30,9 +30,14 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
   const int chunks = (int)((s.len + kL - 1) / kL);
   const size_t state = ((size_t)n * a.H + h) * a.K * a.V;
   const int ra = lane >> 2, ca = 2 * (lane & 3);
-  char* mats = smem + L::chunks * L::chunk;
-  char* ex = mats + L::matrices + local * L::tile;
+  char* ex = smem + L::tiles + local * L::tile;
   float* inv = reinterpret_cast<float*>(ex + L::inv);
+
+  constexpr bool copies = kCopyWarps<TN> == 0;
+  if (!copies && warp >= kQuarter * TN) {
+    copy_ahead<T, KP, TN, true, true>(a, s, chunks, h, col0, keys, records, smem_u32(smem));
+    return;
+  }
 
   float D[2 * KS][4];
 #pragma unroll
@@ -42,15 +47,11 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
       const int col = ra + (e >> 1) * 8, key = w * (KP / 4) + 8 * j + ca + (e & 1);
       D[j][e] = a.dS && col < cols && key < a.K ? a.dS[state + (size_t)key * a.V + v0 + col] : 0.f;
     }
-  auto slot = [&](int c) { return smem + (L::chunks == 2 ? (c & 1) * L::chunk : 0); };
-  if (chunks > 0) {
-    fetch_chunk<T, KP, TN, true>(a, s, s.slot + chunks - 1, h, chunks - 1, col0, keys, records, smem_u32(slot(chunks - 1)));
-    cp_commit();
-  }
+  if (copies && chunks > 0) fetch_all<T, KP, TN, true>(a, s, chunks - 1, h, col0, keys, records, smem_u32(smem));
   for (int c = chunks - 1; c >= 0; --c) {
     const long long rec = s.slot + c;
     const size_t base = ((size_t)rec * a.H + h) * tiles + tile;
-    char* st = slot(c);
+    char *st = smem + L::at(c), *mats = smem + L::mats(c);
     const float* fac = reinterpret_cast<const float*>(st + L::factors);
     {
       const Scale sc = scale_of(tile_max(D));
@@ -84,22 +85,17 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
         }
       }
     }
-    cp_wait<0>();
+    if (copies) cp_wait<0>();
     __syncthreads();  // the chunk has come, dS is in exchange, and nobody is in the chunk behind
-    fetch_matrices<true, threads>(a, rec, h, records, smem_u32(mats));
-    cp_commit();
-    if (L::chunks == 2) {
-      if (c > 0) fetch_chunk<T, KP, TN, true>(a, s, rec - 1, h, c - 1, col0, keys, records, smem_u32(slot(c - 1)));
+    if (copies && !L::ahead) {
+      fetch_matrices<true, TN>(a, rec, h, records, smem_u32(mats));
       cp_commit();
     }
-    if (live && c > 0) {  // on its way to L2 for the chunk before: a quarter of the state and of Z' there
-      const char* state_at = kept.S + ((((size_t)(rec + n)) * a.H + h) * tiles + tile) * 2 * 16 * KP * 2;
-      const char* z_at = (const char*)(kept.Z + (base - (size_t)a.H * tiles) * 16 * kL);
-      constexpr int lines = 2 * 16 * KP * 2 / 128 / kQuarter;
-      if (lane < lines)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(state_at + (w * lines + lane) * 128));
-      else if (lane < lines + 8)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(z_at + (w * 8 + lane - lines) * 128));
+    if (copies && L::chunks == 2) {
+      if (c > 0)
+        fetch_all<T, KP, TN, true>(a, s, c - 1, h, col0, keys, records, smem_u32(smem));
+      else
+        cp_commit();
     }
     // this quarter's share of dO by P's scale, and gam dO
     float x[2][4], y[2][4];
@@ -128,8 +124,11 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
       for (int r = 0; r < 2; ++r)
         zp[j][r] = live ? *reinterpret_cast<const float2*>(kept.Z + (base * 16 + ra + 8 * r) * kL + w * 16 + 8 * j + ca)
                         : make_float2(0.f, 0.f);
-    cp_wait<L::chunks == 2 ? 1 : 0>();
-    __syncthreads();  // R and P have come, dO is in exchange, dS has been read
+    if (copies && !L::ahead) cp_wait<L::chunks == 2 ? 1 : 0>();
+    if (L::ahead)
+      tile_barrier(local);  // dO is in exchange, dS has been read
+    else
+      __syncthreads();  // and R and P have come
     by_tokens<true, NP, 2>(y, ex + L::fu, inv + 2 * kQuarter, smem_u32(mats) + 2 * kTile, w, lane);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -188,8 +187,7 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_back_kernel(const GdrA
     to_state<KP, NP>(D, 1.f, ex + L::fw, inv + 3 * kQuarter, smem_u32(st), w, lane);
     if (L::chunks == 1 && c > 0) {
       __syncthreads();
-      fetch_chunk<T, KP, TN, true>(a, s, rec - 1, h, c - 1, col0, keys, records, smem_u32(smem));
-      cp_commit();
+      if (copies) fetch_all<T, KP, TN, true>(a, s, c - 1, h, col0, keys, records, smem_u32(smem));
     }
   }
   if (a.dS0) {
@@ -531,7 +529,7 @@ cudaError_t launch_back(const GdrArgs& a, const char* keys, const char* records,
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int tiles = (a.V + 15) / 16;
-  kernel<<<dim3((tiles + TN - 1) / TN, a.H, a.N), 32 * kQuarter * TN, smem, stream>>>(a, keys, records, kept);
+  kernel<<<dim3((tiles + TN - 1) / TN, a.H, a.N), kWalkThreads<TN>, smem, stream>>>(a, keys, records, kept);
   return cudaGetLastError();
 }
 

@@ -38,8 +38,12 @@ cudaError_t launch_tc_walk(const GdrArgs& a, const char* keys, const char* recor
 template <typename T, int KP, bool P2>
 cudaError_t launch_prep(const GdrArgs& a, char* keys, char* records, cudaStream_t stream);
 
+// Blocks on an SM: two, where their shared memory lets them.
+template <typename T, int KP, int TN>
+constexpr int kWalkBlocks = sizeof(T) == 2 && KP == 64 && TN <= 2 ? 2 : 1;
+
 // Shared memory of a pass with TN tiles a block: one or two chunks' k, q, columns of v (and dO) and factors,
-// one chunk's R and P, and the tiles' operands in exchange.
+// one or two chunks' R and P, and the tiles' operands in exchange.
 template <typename T, int KP, int TN, bool GRAD>
 struct Stage {
   static constexpr int NP = sizeof(T) == 4 ? 2 : 1;
@@ -61,18 +65,35 @@ struct Stage {
   static constexpr int tile = inv + 5 * kQuarter * 4 + 48;     // a multiple of 128
   static constexpr int least = chunk + matrices + TN * tile;
   static constexpr int chunks = least + chunk <= 227 * 1024 ? 2 : 1;
-  static constexpr int bytes = least + (chunks - 1) * chunk;
+  static constexpr bool ahead = least + chunk + matrices <= 227 * 1024 / kWalkBlocks<T, KP, TN> - 1024;  // R and P twice
+  static constexpr int bytes = least + (chunks - 1) * chunk + (ahead ? matrices : 0);
+  // where chunk c and its R and P lie
+  __host__ __device__ static constexpr int at(int c) { return chunks == 2 ? (c & 1) * chunk : 0; }
+  __host__ __device__ static constexpr int mats(int c) { return chunks * chunk + (ahead ? (c & 1) * matrices : 0); }
+  static constexpr int tiles = chunks * chunk + (ahead ? 2 : 1) * matrices;
   static_assert(tile % 128 == 0, "operands keep their alignment");
   static_assert(bytes <= 227 * 1024, "a block's shared memory");
 };
 
-// Copies the k, q, v, dO and factors of one chunk: every thread a share, 16 bytes at a time.
+// Warps that only copy.  With one or two tiles a block a scheduler has one or two warps that compute, and
+// copies of theirs (some 30 instructions a thread and chunk) would lengthen the chain; with four, registers
+// leave no room for more warps and the others hide them.
+template <int TN>
+constexpr int kCopyWarps = TN == 1 ? 4 : TN == 2 ? 2 : 0;
+template <int TN>
+constexpr int kWalkThreads = 32 * (kQuarter * TN + kCopyWarps<TN>);
+template <int TN>
+constexpr int kCopyThreads = kCopyWarps<TN> ? 32 * kCopyWarps<TN> : kWalkThreads<TN>;
+template <int TN>
+__device__ __forceinline__ int copy_thread() { return kCopyWarps<TN> ? threadIdx.x - 32 * kQuarter * TN : threadIdx.x; }
+
+// Copies the k, q, v, dO and factors of one chunk: every copying thread a share, 16 bytes at a time.
 template <typename T, int KP, int TN, bool GRAD>
 __device__ __forceinline__ void fetch_chunk(const GdrArgs& a, const Seq& s, long long rec, int h, int c, int col0,
                                             const char* keys, const char* records, uint32_t to) {
   using L = Stage<T, KP, TN, GRAD>;
-  const int tid = threadIdx.x;
-  constexpr int threads = 32 * kQuarter * TN;
+  const int tid = copy_thread<TN>();
+  constexpr int threads = kCopyThreads<TN>;
   const char* k = keys + (rec * a.HK + h / (a.H / a.HK)) * keys_bytes(KP, L::NP);
   for (int i = tid; i < keys_bytes(KP, L::NP) / 16; i += threads) cp_async16(to + i * 16, k + i * 16, true);
   const char* f = records + (rec * a.H + h) * record_bytes(L::P2) + L::matrices;
@@ -90,10 +111,43 @@ __device__ __forceinline__ void fetch_chunk(const GdrArgs& a, const Seq& s, long
   }
 }
 // and its R and P
-template <bool P2, int THREADS>
+template <bool P2, int TN>
 __device__ __forceinline__ void fetch_matrices(const GdrArgs& a, long long rec, int h, const char* records, uint32_t to) {
   const char* r = records + (rec * a.H + h) * record_bytes(P2);
-  for (int i = threadIdx.x; i < (record_bytes(P2) - kFactorBytes) / 16; i += THREADS) cp_async16(to + i * 16, r + i * 16, true);
+  for (int i = copy_thread<TN>(); i < (record_bytes(P2) - kFactorBytes) / 16; i += kCopyThreads<TN>)
+    cp_async16(to + i * 16, r + i * 16, true);
+}
+// A chunk with all that is copied ahead of it.
+template <typename T, int KP, int TN, bool GRAD>
+__device__ __forceinline__ void fetch_all(const GdrArgs& a, const Seq& s, int c, int h, int col0, const char* keys,
+                                          const char* records, uint32_t smem) {
+  using L = Stage<T, KP, TN, GRAD>;
+  fetch_chunk<T, KP, TN, GRAD>(a, s, s.slot + c, h, c, col0, keys, records, smem + L::at(c));
+  if (L::ahead) fetch_matrices<L::P2, TN>(a, s.slot + c, h, records, smem + L::mats(c));
+  cp_commit();
+}
+// The copying warps' part of a pass, forward or from the last chunk on: the same barriers as the others'.
+template <typename T, int KP, int TN, bool GRAD, bool BACK>
+__device__ __forceinline__ void copy_ahead(const GdrArgs& a, const Seq& s, int chunks, int h, int col0, const char* keys,
+                                           const char* records, uint32_t smem) {
+  using L = Stage<T, KP, TN, GRAD>;
+  auto fetch = [&](int i) {
+    if (i < chunks) fetch_all<T, KP, TN, GRAD>(a, s, BACK ? chunks - 1 - i : i, h, col0, keys, records, smem);
+  };
+  fetch(0);
+  for (int i = 0; i < chunks; ++i) {
+    const int c = BACK ? chunks - 1 - i : i;
+    cp_wait<0>();
+    __syncthreads();
+    if (!L::ahead) {  // (the next chunk's copies would hold these up)
+      fetch_matrices<L::P2, TN>(a, s.slot + c, h, records, smem + L::mats(c));
+      cp_commit();
+      cp_wait<0>();
+      __syncthreads();
+    }
+    if (L::chunks == 1 && i + 1 < chunks) __syncthreads();
+    fetch(i + 1);
+  }
 }
 
 // A quarter's 16 columns x 16 tokens of a tile [64][16 TN] in shared memory, as accumulator tiles.
@@ -270,10 +324,10 @@ __device__ __forceinline__ void to_state(float (&S)[KP / 32][4], float keep, con
 
 // A block takes 16 TN value columns of one value head of one sequence.
 template <typename T, int KP, int TN, bool GRAD>
-__global__ void __launch_bounds__(32 * kQuarter * TN) gdr_walk_kernel(const GdrArgs a, const char* keys,
+__global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_walk_kernel(const GdrArgs a, const char* keys,
                                                                       const char* records, const Kept kept) {
   using L = Stage<T, KP, TN, GRAD>;
-  constexpr int NP = L::NP, NK = kept_parts<T>(), KS = KP / 64, threads = 32 * kQuarter * TN;
+  constexpr int NP = L::NP, NK = kept_parts<T>(), KS = KP / 64;
   constexpr bool FINE = L::P2;  // the output in fp32 accuracy: two parts of S, U and P under it
   extern __shared__ __align__(128) char smem[];
   const int n = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -285,9 +339,14 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_walk_kernel(const GdrA
   const int chunks = (int)((s.len + kL - 1) / kL);
   const size_t state = ((size_t)n * a.H + h) * a.K * a.V;
   const int ra = lane >> 2, ca = 2 * (lane & 3);  // row and first column of this lane in an accumulator
-  char* mats = smem + L::chunks * L::chunk;
-  char* ex = mats + L::matrices + local * L::tile;
+  char* ex = smem + L::tiles + local * L::tile;
   float* inv = reinterpret_cast<float*>(ex + L::inv);
+
+  constexpr bool copies = kCopyWarps<TN> == 0;  // the warps that compute copy as well
+  if (!copies && warp >= kQuarter * TN) {
+    copy_ahead<T, KP, TN, GRAD, false>(a, s, chunks, h, col0, keys, records, smem_u32(smem));
+    return;
+  }
 
   float S[2 * KS][4];  // keys w KP / 4 ..
 #pragma unroll
@@ -313,28 +372,28 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_walk_kernel(const GdrA
     }
   };
 
-  if (chunks > 0) {
-    fetch_chunk<T, KP, TN, GRAD>(a, s, s.slot, h, 0, col0, keys, records, smem_u32(smem));
-    cp_commit();
-  }
+  if (copies && chunks > 0) fetch_all<T, KP, TN, GRAD>(a, s, 0, h, col0, keys, records, smem_u32(smem));
   for (int c = 0; c < chunks; ++c) {
     const long long rec = s.slot + c;
     const size_t base = ((size_t)rec * a.H + h) * tiles + tile;
-    char* st = smem + (L::chunks == 2 ? (c & 1) * L::chunk : 0);
+    char *st = smem + L::at(c), *mats = smem + L::mats(c);
     const float* fac = reinterpret_cast<const float*>(st + L::factors);
     {
       const Scale sc = scale_of(tile_max(S));
       give<KS, 2>(S, sc, ex + L::fs, inv, w, lane);
       keep_state(rec + n, sc);
     }
-    cp_wait<0>();
+    if (copies) cp_wait<0>();
     __syncthreads();  // the chunk has come, the states are in exchange, and nobody is in the chunk before
-    fetch_matrices<L::P2, threads>(a, rec, h, records, smem_u32(mats));
-    cp_commit();
-    if (L::chunks == 2) {
-      if (c + 1 < chunks)
-        fetch_chunk<T, KP, TN, GRAD>(a, s, rec + 1, h, c + 1, col0, keys, records, smem_u32(smem) + ((c + 1) & 1) * L::chunk);
+    if (copies && !L::ahead) {
+      fetch_matrices<L::P2, TN>(a, rec, h, records, smem_u32(mats));
       cp_commit();
+    }
+    if (copies && L::chunks == 2) {
+      if (c + 1 < chunks)
+        fetch_all<T, KP, TN, GRAD>(a, s, c + 1, h, col0, keys, records, smem_u32(smem));
+      else
+        cp_commit();
     }
     // Z = V - gam (K S), O = gam (Q S)
     float x[2][4], o[2][4], z[2][4], u[2][4];
@@ -353,8 +412,11 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_walk_kernel(const GdrA
       }
     }
     give<1, 2>(u, scale_of(tile_max(u)), ex + L::fz, inv + kQuarter, w, lane);
-    cp_wait<L::chunks == 2 ? 1 : 0>();
-    __syncthreads();  // R and P have come, beta Z is in exchange
+    if (copies && !L::ahead) cp_wait<L::chunks == 2 ? 1 : 0>();
+    if (L::ahead)
+      tile_barrier(local);  // beta Z is in exchange
+    else
+      __syncthreads();  // and R and P have come
     // Z' = Z + R (beta Z), U = beta Z'
     by_tokens<false, 2, 2>(x, ex + L::fz, inv + kQuarter, smem_u32(mats), w, lane);
     float uw[2][4];
@@ -413,8 +475,7 @@ __global__ void __launch_bounds__(32 * kQuarter * TN) gdr_walk_kernel(const GdrA
     to_state<KP, NP>(S, fac[kGam * kL + kL - 1], ex + L::fw, inv + 3 * kQuarter, smem_u32(st), w, lane);
     if (L::chunks == 1 && c + 1 < chunks) {
       __syncthreads();
-      fetch_chunk<T, KP, TN, GRAD>(a, s, rec + 1, h, c + 1, col0, keys, records, smem_u32(smem));
-      cp_commit();
+      if (copies) fetch_all<T, KP, TN, GRAD>(a, s, c + 1, h, col0, keys, records, smem_u32(smem));
     }
   }
   if constexpr (GRAD) keep_state(s.slot + chunks + n, scale_of(tile_max(S)));
@@ -468,7 +529,7 @@ cudaError_t launch_walk_tn(const GdrArgs& a, const char* keys, const char* recor
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int tiles = (a.V + 15) / 16;
-  kernel<<<dim3((tiles + TN - 1) / TN, a.H, a.N), 32 * kQuarter * TN, smem, stream>>>(a, keys, records, kept);
+  kernel<<<dim3((tiles + TN - 1) / TN, a.H, a.N), kWalkThreads<TN>, smem, stream>>>(a, keys, records, kept);
   return cudaGetLastError();
 }
 
