@@ -15,7 +15,7 @@ namespace {
 
 // A block takes 16 TN value columns of one value head of one sequence, chunks from the last to the first.
 template <typename T, int KP, int TN>
-__global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_back_kernel(const GdrArgs a, const char* keys,
+__global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN, true>) gdr_back_kernel(const GdrArgs a, const char* keys,
                                                                       const char* records, const Kept kept) {
   using L = Stage<T, KP, TN, true>;
   constexpr int NP = L::NP, NK = kept_parts<T>(), KS = KP / 64;
@@ -547,7 +547,7 @@ cudaError_t backward(const GdrArgs& a, char* ws, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_walk<T, KP, true>(a, keys, records, k, stream);
   if (e != cudaSuccess) return e;
-  const int tn = tiles_a_block(a);
+  const int tn = tiles_a_block(a, true);
   if constexpr (sizeof(T) == 2)
     if (tn == 4) e = launch_back<T, KP, 4>(a, keys, records, k, stream);
   if (tn != 4) e = tn == 2 ? launch_back<T, KP, 2>(a, keys, records, k, stream) : launch_back<T, KP, 1>(a, keys, records, k, stream);

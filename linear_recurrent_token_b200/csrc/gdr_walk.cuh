@@ -39,8 +39,8 @@ template <typename T, int KP, bool P2>
 cudaError_t launch_prep(const GdrArgs& a, char* keys, char* records, cudaStream_t stream);
 
 // Blocks on an SM: two, where their shared memory lets them.
-template <typename T, int KP, int TN>
-constexpr int kWalkBlocks = sizeof(T) == 2 && KP == 64 && TN <= 2 ? 2 : 1;
+template <typename T, int KP, int TN, bool GRAD>
+constexpr int kWalkBlocks = sizeof(T) == 2 && KP == 64 && (TN == 1 || (TN == 2 && !GRAD)) ? 2 : 1;
 
 // Shared memory of a pass with TN tiles a block: one or two chunks' k, q, columns of v (and dO) and factors,
 // one or two chunks' R and P, and the tiles' operands in exchange.
@@ -65,7 +65,7 @@ struct Stage {
   static constexpr int tile = inv + 5 * kQuarter * 4 + 48;     // a multiple of 128
   static constexpr int least = chunk + matrices + TN * tile;
   static constexpr int chunks = least + chunk <= 227 * 1024 ? 2 : 1;
-  static constexpr bool ahead = least + chunk + matrices <= 227 * 1024 / kWalkBlocks<T, KP, TN> - 1024;  // R and P twice
+  static constexpr bool ahead = least + chunk + matrices <= 227 * 1024 / kWalkBlocks<T, KP, TN, GRAD> - 1024;  // R and P twice
   static constexpr int bytes = least + (chunks - 1) * chunk + (ahead ? matrices : 0);
   // where chunk c and its R and P lie
   __host__ __device__ static constexpr int at(int c) { return chunks == 2 ? (c & 1) * chunk : 0; }
@@ -324,7 +324,7 @@ __device__ __forceinline__ void to_state(float (&S)[KP / 32][4], float keep, con
 
 // A block takes 16 TN value columns of one value head of one sequence.
 template <typename T, int KP, int TN, bool GRAD>
-__global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_walk_kernel(const GdrArgs a, const char* keys,
+__global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN, GRAD>) gdr_walk_kernel(const GdrArgs a, const char* keys,
                                                                       const char* records, const Kept kept) {
   using L = Stage<T, KP, TN, GRAD>;
   constexpr int NP = L::NP, NK = kept_parts<T>(), KS = KP / 64;
@@ -492,33 +492,33 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
 
 // What a pass over 32 chunks would take with blocks of 16 TN columns (TN = 0: the tcgen05 pass, 128 columns), in
 // us.  A block's chunks are one chain, longer the more columns it has; blocks beyond the 148 SMs make a
-// further round of it.  For bf16 keys of up to 64 two blocks of one or two tiles share an SM and each other's
-// waits.  Sequences of one length go round in whole rounds; packed ones are uneven (their lengths are not known on
-// the host): shorter ones make room, so count half of them, and no fewer than the longest one's chain.
-// The chains are measured (T = 2048, one block an SM: 80, 105, 160, 165 us for 128 keys; 72, 95, 140, 165
-// for 64), and so is what follows from them; us with the preparation, TN = 1 / 2 / 4 / tcgen05:
-//   128 x 128, 16 heads 106/133/188/194, 32: 196/153/208/215, 64: 371/286/245/250, 80: 458/402/416/268,
-//   128: 657/557/474/327, 256: 1294/999/926/633;   128 x 256, 32 heads 336/252/210/219, 48: 493/366/381/238
-//   64 x 64, 16 heads 90/108/145/178, 64: 156/154/189/227, 128: 295/259/255/295, 256: 565/498/493/560
-//   64 x 128, 32 heads 126/123/161/187, 64: 230/195/191/218, 80: 319/282/320/231, 128: 446/376/372/280
-//   64 x 128 packed, 13 uneven sequences of 6007 tokens, 4 heads 82/103/102/121, 8: 114/116/116/129, 16: 194/175/186/176
-//   gradients 128 x 128, 16 heads 325/398/598, 64: 1217/917/812, 96: 1800/1351/1450, 128: 2175/1790/1593
-inline double walk_cost(const GdrArgs& a, int TN) {
-  const bool two = a.dtype == 1 && a.K <= 64 && (TN == 1 || TN == 2);
+// further round of it.  Where two blocks fit an SM they share each other's waits.  Sequences of one length go
+// round in whole rounds; packed ones are uneven (their lengths are not known on the host): shorter ones
+// make room, so count half of them, and no fewer than the longest one's chain.
+// The chains are fitted to what was measured; us with the preparation, 2048 tokens, TN = 1 / 2 / 4 / tcgen05:
+//   128 x 128, 16 heads 84/109/184/186, 32: 153/124/199/202, 64: 290/231/224/229, 80: 358/325/398/243,
+//   128: 510/446/437/284, 256: 990/789/850/545;   128 x 256, 32 heads 262/204/199/206, 48: 384/300/371/224
+//   64 x 64, 16 heads 73/95/145/173, 64: 127/143/179/207, 128: 237/212/221/253, 256: 458/410/428/483
+//   64 x 128, 32 heads 106/110/156/175, 64: 193/167/178/197, 80: 273/253/311/208, 128: 373/319/341/240
+//   64 x 128 packed, 13 uneven sequences of 6007 tokens, 4 heads 77/94/105/120, 8: 101/114/114/123, 16: 163/170/176/161
+//   gradients 128 x 128, 16 heads 294/370/596, 64: 1100/848/797, 96: 1629/1249/1433, 128: 1965/1652/1560;
+//   64 x 64, 64 heads 422/437/558, 128: 819/858/724
+inline double walk_cost(const GdrArgs& a, int TN, bool grad) {
+  const bool narrow = a.dtype == 1 && a.K <= 64, two = narrow && (TN == 1 || (TN == 2 && !grad));
   const int columns = TN ? 16 * TN : 128;
   const long long blocks = (long long)a.N * a.H * ((a.V + columns - 1) / columns);
-  const double chain = TN == 0 ? 165 : a.dtype == 1 && a.K <= 64 ? (TN == 1 ? 72 : TN == 2 ? 95 : 140) : (TN == 1 ? 80 : TN == 2 ? 105 : 160);
-  const double pair = two ? (TN == 1 ? 115 : 165) : 2 * chain;  // two blocks on one SM
+  const double chain = TN == 0 ? (narrow ? 170 : 172) : TN == 1 ? (narrow ? 66 : 68) : TN == 2 ? (narrow ? 98 : 95) : narrow ? 158 : 168;
+  const double pair = two ? (TN == 1 ? 98 : 155) : 2 * chain;  // two blocks on one SM
   if (a.packed) return std::max(chain, 0.5 * blocks / 148 * pair / 2);
   const long long rounds = (blocks + 147) / 148;
   return rounds / 2 * pair + rounds % 2 * chain;
 }
 
 // The tiles a block, by that cost (fp32 inputs: at most two; their second parts fill the registers).
-inline int tiles_a_block(const GdrArgs& a) {
+inline int tiles_a_block(const GdrArgs& a, bool grad) {
   int best = 1;
   for (int TN = 2; TN <= (a.dtype == 1 ? 4 : 2); TN *= 2)
-    if (walk_cost(a, TN) < walk_cost(a, best)) best = TN;
+    if (walk_cost(a, TN, grad) < walk_cost(a, best, grad)) best = TN;
   return best;
 }
 
@@ -535,7 +535,7 @@ cudaError_t launch_walk_tn(const GdrArgs& a, const char* keys, const char* recor
 
 template <typename T, int KP, bool GRAD>
 cudaError_t launch_walk(const GdrArgs& a, const char* keys, const char* records, const Kept& kept, cudaStream_t stream) {
-  const int tn = tiles_a_block(a);
+  const int tn = tiles_a_block(a, GRAD);
   if constexpr (sizeof(T) == 2)
     if (tn == 4) return launch_walk_tn<T, KP, 4, GRAD>(a, keys, records, kept, stream);
   return tn == 2 ? launch_walk_tn<T, KP, 2, GRAD>(a, keys, records, kept, stream)

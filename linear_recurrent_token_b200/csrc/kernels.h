@@ -167,10 +167,10 @@ struct GdrArgs {
 };
 cudaError_t launch_gdr_recurrent(const GdrArgs& a, cudaStream_t stream);
 // chunks of 64 tokens on the tensor cores (gdr_chunk.cu).  Automatic calls take them from this many tokens a row
-// on; us, token by token / chunks: bf16 128 x 128, 16 heads, 24 tokens 20/24, 32: 24/24, 64: 38/25; 512 heads, 16 tokens
-// 81/67, 32: 134/70; fp32 128 x 128, 64 heads, 24: 24/26, 48: 38/26; bf16 64 x 64, 16 heads, 32: 20/24, 48: 24/23.
+// on; us, token by token / chunks: bf16 128 x 128, 16 heads, 24 tokens 20/25, 32: 23/24, 64: 38/24; 512 heads, 16 tokens
+// 81/61, 32: 134/63; fp32 128 x 128, 64 heads, 24: 24/27, 48: 38/28; bf16 64 x 64, 16 heads, 32: 20/24, 48: 24/24.
 // Packed rows whose sequences have fewer than 8 tokens on average stay token by token (256 sequences of
-// one token, 16 heads 128 x 128: 207/416).
+// one token, 16 heads 128 x 128: 206/381).
 constexpr int kGdrChunkFrom = 32, kGdrChunkAverage = 8;
 // Head of the chunk kernels' workspace: its first word is the error word of the tcgen05 pass (1: a wait ran
 // out).  gdr_tc_pass: whether a call runs that pass (known from its sizes).
