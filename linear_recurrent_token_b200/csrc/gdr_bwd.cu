@@ -218,8 +218,9 @@ struct GradStage {
   // dP o D by k's and q's scales and dW o D by k's, rows and columns, take the place of a head's last columns
   static constexpr int mats = 4 * NP * kTile;
   static constexpr int block = ds + NP * kVB * KP * 2 > mats ? ds + NP * kVB * KP * 2 : mats;
-  // factors; scales of the operands in work as powers of two at most 1: [5][4 tiles][4], and their largest
-  static constexpr int small = kFactorBytes + 5 * 16 * 4 + 8 * 4 + kGradThreads / 32 * 4 * 4;
+  // factors and the operands' scales [5][4 tiles][4], twice; the scales in work as powers of two at most 1, and
+  // their largest
+  static constexpr int small = 2 * kFactorBytes + 3 * 5 * 16 * 4 + 8 * 4 + kGradThreads / 32 * 4 * 4;
   static constexpr int blocks = cols + 2 * block + small <= 227 * 1024 ? 2 : 1;
   static constexpr int bytes = cols + blocks * block + small;
   static_assert(bytes <= 227 * 1024, "a block's shared memory");
@@ -269,8 +270,9 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
   using L = GradStage<T, KP>;
   constexpr int NP = L::NP, NK = kept_parts<T>(), NT = KP / 32;
   extern __shared__ __align__(128) char smem[];
-  float* fac = reinterpret_cast<float*>(smem + L::cols + L::blocks * L::block);
-  float* rel = fac + kFactors * kL;  // [operand][tile][quarter]
+  float* const factors = reinterpret_cast<float*>(smem + L::cols + L::blocks * L::block);  // [2][kFactors][64]
+  float* const scales = factors + 2 * kFactors * kL;                                       // [2][operand][tile][quarter]
+  float* rel = scales + 2 * 5 * 16;  // [operand][tile][quarter]
   float* top = rel + 5 * 16;
   float* most = top + 8;  // [16 warps][4]
   int n, c;
@@ -308,6 +310,18 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
     operand(kept.U, base, NK, L::u, kL);
     operand(kept.S, sbase, 2, L::s, KP);
     operand(kept.D, base, NK, L::ds, KP);
+    if (tid < 5 * 4) {  // the scales, a tile's four a thread
+      const float* invs[5] = {kept.dO_inv, kept.dV_inv, kept.U_inv, kept.S_inv, kept.D_inv};
+      const int of = tid >> 2, tile = tid & 3;
+      const bool in = tile < live;
+      cp_async16(smem_u32(scales + ((i & 1) * 5 + of) * 16 + tile * 4),
+                 invs[of] + ((of == 3 ? sbase : base) + (in ? tile : 0)) * kQuarter, in);
+    }
+    if (i % parts == 0) {
+      const char* fin = records + (rec * a.H + h) * record_bytes(true) + 4 * kTile;
+      const uint32_t to_fac = smem_u32(factors + (i / parts & 1) * kFactors * kL);
+      for (int e = tid; e < kFactorBytes / 16; e += kGradThreads) cp_async16(to_fac + e * 16, fin + e * 16, true);
+    }
     cp_commit();
   };
 
@@ -319,15 +333,10 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
     cp_wait<0>();
     __syncthreads();  // these columns have come; the ones before, and a head's matrices and factors, are done with
     if (L::blocks == 2 && i + 1 < total) fetch(i + 1);
-    if (part == 0) {
-      const float* fin = reinterpret_cast<const float*>(records + (rec * a.H + h) * record_bytes(true) + 4 * kTile);
-      for (int e = tid; e < kFactors * kL; e += kGradThreads) fac[e] = fin[e];
-      zero(dP), zero(dW);
-    }
+    const float* fac = factors + (i / parts & 1) * kFactors * kL;
+    if (part == 0) zero(dP), zero(dW);
     if (tid < 5 * 32) {  // a warp an operand: its 16 scales against their largest
-      const float* invs[5] = {kept.dO_inv, kept.dV_inv, kept.U_inv, kept.S_inv, kept.D_inv};
-      const size_t at = ((size_t)(warp == 3 ? rec + n : rec) * a.H + h) * tiles + part * 4 + (lane >> 2);
-      const float x = lane < 16 && part * 4 + (lane >> 2) < tiles ? invs[warp][at * kQuarter + (lane & 3)] : 0.f;
+      const float x = lane < 16 ? scales[((i & 1) * 5 + warp) * 16 + lane] : 0.f;
       const float big = warp_max(x);
       if (lane < 16) rel[warp * 16 + lane] = big > 0.f ? x / big : 0.f;
       if (lane == 0) top[warp] = big;
