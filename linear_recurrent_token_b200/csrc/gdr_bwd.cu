@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
   zero(dq), zero(dk);
   fetch(0);
   for (int i = 0; i < total; ++i) {
-    const int h = hk * group + i / parts, part = i % parts;
+    const int part = i % parts;
     cp_wait<0>();
     __syncthreads();  // these columns have come; the ones before, and a head's matrices and factors, are done with
     if (L::blocks == 2 && i + 1 < total) fetch(i + 1);
