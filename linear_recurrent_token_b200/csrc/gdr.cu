@@ -139,13 +139,19 @@ cudaError_t launch_rec(const GdrArgs& a, cudaStream_t stream) {
 // Decode step.  CW lanes cover 4 CW neighbouring value columns of a state row with 16-byte
 // accesses, 256 / CW rows at a time; every load of a thread (NR rows) is in flight before the first
 // is used, and one pass over shared memory joins both products.  Bound by HBM: the state is read
-// and written once, 8 K V bytes a head.  256 rows of 16 heads of 128 x 128, six of them padding: 95 us for
-// 529 MB, 5.6 TB/s, 85 % of a copy's rate; one row: 3.3 us, latency.  (The tile in shared memory, three
-// blocks on an SM instead of two, took 106 us.)
+// and written once, 8 K V bytes a head.  256 rows of 16 heads of 128 x 128, six of them padding, 529 MB: 94 us
+// in a loop from Python, 5.6 TB/s, 85 % of a copy's rate, 88 in a graph; one row: 3.3 us, latency.  (The
+// tile in shared memory, three blocks on an SM instead of two, took 10 us more.)
 //
 // Rows of the batch that name the same slot are taken one after the other in the batch's order by
 // the block of the first of them; a slot outside 0 .. pool - 1 marks padding (o = 0).
 constexpr int kStepThreads = 256;
+// A block sends for the state of the head this many blocks behind it, as far as L2: that its own loads wait for
+// its slot, and its stores for its sums, then leaves memory busy.  256 rows of 16 heads of 128 x 128, slots
+// given: without 102 us, 148 ahead 92, 296 93, 592 93; no slots 94, 87, 88, 88.  Not for heads below 64 KB, more
+// of which share an SM (4096 of 64 x 64: 27 without, 29 with; 2048 of 64 x 128: 21.4/22.4), nor beyond 256 KB,
+// which fill memory's queues by themselves (4096 of 128 x 256, between the two: 175/168).
+constexpr int kStepAhead = 148, kStepLeast = 16384, kStepMost = 65536;
 
 template <typename T, int CW, int NR>
 __global__ void __launch_bounds__(kStepThreads) gdr_step_kernel(const GdrStepArgs a) {
@@ -172,6 +178,14 @@ __global__ void __launch_bounds__(kStepThreads) gdr_step_kernel(const GdrStepArg
     const int row = i * RP + rp;
     S[i] = in && row < a.K ? __ldcs(reinterpret_cast<const float4*>(state + (size_t)row * a.V))
                            : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  if (tid == kStepThreads - 1 && blockIdx.x == 0 && a.K * a.V >= kStepLeast && a.K * a.V <= kStepMost) {
+    const long long ahead = (long long)b0 * a.H + h + max(1, kStepAhead / (int)gridDim.x), row = ahead / a.H;
+    const long long at = row >= a.B ? -1 : a.slots ? (long long)a.slots[row] : row;
+    if (at >= 0 && at < a.pool)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.S + ((size_t)at * a.H + ahead % a.H) * a.K * a.V),
+                   "r"(a.K * a.V * 4)
+                   : "memory");
   }
   if (tid == 0) first = 1, next = a.B;
   for (int b = b0; b < a.B;) {
