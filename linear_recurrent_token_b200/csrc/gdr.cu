@@ -279,16 +279,18 @@ void launch_step_cw(const GdrStepArgs& a, cudaStream_t stream) {
   constexpr int RP = kStepThreads / CW;
   const dim3 grid((a.V + 4 * CW - 1) / (4 * CW), a.H, a.B);
   const int nr = (a.K + RP - 1) / RP;
-  if (nr <= 2)
+  if (nr <= 2) {
     gdr_step_kernel<T, CW, 2><<<grid, kStepThreads, 0, stream>>>(a);
-  else if (nr <= 4)
+  } else if (nr <= 4) {
     gdr_step_kernel<T, CW, 4><<<grid, kStepThreads, 0, stream>>>(a);
-  else if (nr <= 8)
+  } else if (nr <= 8) {
     gdr_step_kernel<T, CW, 8><<<grid, kStepThreads, 0, stream>>>(a);
-  else if (nr <= 16)
+  } else if constexpr (RP < 32) {  // K is at most 256
+    if constexpr (RP < 16) {
+      if (nr > 16) return gdr_step_kernel<T, CW, 32><<<grid, kStepThreads, 0, stream>>>(a);
+    }
     gdr_step_kernel<T, CW, 16><<<grid, kStepThreads, 0, stream>>>(a);
-  else
-    gdr_step_kernel<T, CW, 32><<<grid, kStepThreads, 0, stream>>>(a);
+  }
 }
 
 template <typename T>

@@ -17,7 +17,7 @@ namespace {
 // chain as the forward pass's, with six products.  64 heads of 128 x 128, 2048 bf16 tokens, TN = 4: 300 us, 9.4 us
 // a chunk, issue slots 40 % taken, tensor pipes 23 %.
 template <typename T, int KP, int TN>
-__global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN, true>) gdr_back_kernel(const GdrArgs a, const char* keys,
+__global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_back_kernel(const GdrArgs a, const char* keys,
                                                                       const char* records, const Kept kept) {
   using L = Stage<T, KP, TN, true>;
   constexpr int NP = L::NP, NK = kept_parts<T>(), KS = KP / 64;
@@ -561,10 +561,12 @@ cudaError_t backward(const GdrArgs& a, char* ws, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_walk<T, KP, true>(a, keys, records, k, stream);
   if (e != cudaSuccess) return e;
-  const int tn = tiles_a_block(a, true);
-  if constexpr (sizeof(T) == 2)
+  const int tn = tiles_a_block<T, KP, true>(a);
+  if (tn == 1) e = launch_back<T, KP, 1>(a, keys, records, k, stream);
+  if constexpr (kWalkOf<T, KP, true>(2))
+    if (tn == 2) e = launch_back<T, KP, 2>(a, keys, records, k, stream);
+  if constexpr (kWalkOf<T, KP, true>(4))
     if (tn == 4) e = launch_back<T, KP, 4>(a, keys, records, k, stream);
-  if (tn != 4) e = tn == 2 ? launch_back<T, KP, 2>(a, keys, records, k, stream) : launch_back<T, KP, 1>(a, keys, records, k, stream);
   if (e != cudaSuccess) return e;
   const auto kernel = gdr_grad_kernel<T, KP>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GradStage<T, KP>::bytes);

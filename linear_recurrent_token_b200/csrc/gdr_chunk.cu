@@ -410,7 +410,9 @@ bool gdr_chunk_supported(int K) { return K <= 128; }
 
 // bf16 inputs: whichever pass takes less (walk_cost).
 bool gdr_tc_pass(const GdrArgs& a) {
-  return a.dtype == 1 && gdr::walk_cost(a, 0, false) < gdr::walk_cost(a, gdr::tiles_a_block(a, false), false);
+  if (!a.dtype) return false;
+  const int tn = a.K <= 64 ? gdr::tiles_a_block<__nv_bfloat16, 64, false>(a) : gdr::tiles_a_block<__nv_bfloat16, 128, false>(a);
+  return gdr::walk_cost(a, 0) < gdr::walk_cost(a, tn);
 }
 
 size_t gdr_chunk_workspace_bytes(const GdrArgs& a) {

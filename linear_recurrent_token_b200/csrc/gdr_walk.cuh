@@ -39,8 +39,8 @@ template <typename T, int KP, bool P2>
 cudaError_t launch_prep(const GdrArgs& a, char* keys, char* records, cudaStream_t stream);
 
 // Blocks on an SM: two, where their shared memory lets them.
-template <typename T, int KP, int TN, bool GRAD>
-constexpr int kWalkBlocks = sizeof(T) == 2 && KP == 64 && (TN == 1 || (TN == 2 && !GRAD)) ? 2 : 1;
+template <typename T, int KP, int TN>
+constexpr int kWalkBlocks = sizeof(T) == 2 && KP == 64 && TN <= 2 ? 2 : 1;
 
 // Shared memory of a pass with TN tiles a block: one or two chunks' k, q, columns of v (and dO) and factors,
 // one or two chunks' R and P, and the tiles' operands in exchange.
@@ -65,7 +65,7 @@ struct Stage {
   static constexpr int tile = inv + 5 * kQuarter * 4 + 48;     // a multiple of 128
   static constexpr int least = chunk + matrices + TN * tile;
   static constexpr int chunks = least + chunk <= 227 * 1024 ? 2 : 1;
-  static constexpr bool ahead = least + chunk + matrices <= 227 * 1024 / kWalkBlocks<T, KP, TN, GRAD> - 1024;  // R and P twice
+  static constexpr bool ahead = least + chunk + matrices <= 227 * 1024 / kWalkBlocks<T, KP, TN> - 1024;  // R and P twice
   static constexpr int bytes = least + (chunks - 1) * chunk + (ahead ? matrices : 0);
   // where chunk c and its R and P lie
   __host__ __device__ static constexpr int at(int c) { return chunks == 2 ? (c & 1) * chunk : 0; }
@@ -327,7 +327,7 @@ __device__ __forceinline__ void to_state(float (&S)[KP / 32][4], float keep, con
 // 1.7 us or 3250 cycles a chunk, of which K S and Q S 1000, R and its operands 850, P U 600, the state 450, its
 // parts 230.  64 heads, 2048 tokens, TN = 4 for the gradients: 217 us, issue slots 42 % taken, tensor pipes 33 %.
 template <typename T, int KP, int TN, bool GRAD>
-__global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN, GRAD>) gdr_walk_kernel(const GdrArgs a, const char* keys,
+__global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_walk_kernel(const GdrArgs a, const char* keys,
                                                                       const char* records, const Kept kept) {
   using L = Stage<T, KP, TN, GRAD>;
   constexpr int NP = L::NP, NK = kept_parts<T>(), KS = KP / 64;
@@ -506,8 +506,8 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN, GRAD>
 //   64 x 128 packed, 13 uneven sequences of 6007 tokens, 4 heads 77/94/105/120, 8: 101/114/114/123, 16: 163/170/176/161
 //   gradients 128 x 128, 16 heads 294/370/596, 64: 1100/848/797, 96: 1629/1249/1433, 128: 1965/1652/1560;
 //   64 x 64, 64 heads 422/437/558, 128: 819/858/724
-inline double walk_cost(const GdrArgs& a, int TN, bool grad) {
-  const bool narrow = a.dtype == 1 && a.K <= 64, two = narrow && (TN == 1 || (TN == 2 && !grad));
+inline double walk_cost(const GdrArgs& a, int TN) {
+  const bool narrow = a.dtype == 1 && a.K <= 64, two = narrow && (TN == 1 || TN == 2);
   const int columns = TN ? 16 * TN : 128;
   const long long blocks = (long long)a.N * a.H * ((a.V + columns - 1) / columns);
   const double chain = TN == 0 ? (narrow ? 170 : 172) : TN == 1 ? (narrow ? 66 : 68) : TN == 2 ? (narrow ? 98 : 95) : narrow ? 158 : 168;
@@ -517,11 +517,19 @@ inline double walk_cost(const GdrArgs& a, int TN, bool grad) {
   return rounds / 2 * pair + rounds % 2 * chain;
 }
 
-// The tiles a block, by that cost (fp32 inputs: at most two; their second parts fill the registers).
-inline int tiles_a_block(const GdrArgs& a, bool grad) {
+// The tiles a block, by that cost.  fp32 inputs: at most two; their second parts fill the registers.  With narrow
+// bf16 keys two tiles and two blocks an SM always do better than four and one (above); for the gradients
+// two do not leave an SM room for a second block: one or four.
+template <typename T, int KP, bool GRAD>
+constexpr bool kWalkOf(int TN) {
+  const bool narrow = sizeof(T) == 2 && KP == 64;
+  return TN == 1 || (TN == 2 && !(GRAD && narrow)) || (TN == 4 && sizeof(T) == 2 && (GRAD || !narrow));
+}
+template <typename T, int KP, bool GRAD>
+int tiles_a_block(const GdrArgs& a) {
   int best = 1;
-  for (int TN = 2; TN <= (a.dtype == 1 ? 4 : 2); TN *= 2)
-    if (walk_cost(a, TN, grad) < walk_cost(a, best, grad)) best = TN;
+  for (int TN = 2; TN <= 4; TN *= 2)
+    if (kWalkOf<T, KP, GRAD>(TN) && walk_cost(a, TN) < walk_cost(a, best)) best = TN;
   return best;
 }
 
@@ -538,11 +546,12 @@ cudaError_t launch_walk_tn(const GdrArgs& a, const char* keys, const char* recor
 
 template <typename T, int KP, bool GRAD>
 cudaError_t launch_walk(const GdrArgs& a, const char* keys, const char* records, const Kept& kept, cudaStream_t stream) {
-  const int tn = tiles_a_block(a, GRAD);
-  if constexpr (sizeof(T) == 2)
+  const int tn = tiles_a_block<T, KP, GRAD>(a);
+  if constexpr (kWalkOf<T, KP, GRAD>(4))
     if (tn == 4) return launch_walk_tn<T, KP, 4, GRAD>(a, keys, records, kept, stream);
-  return tn == 2 ? launch_walk_tn<T, KP, 2, GRAD>(a, keys, records, kept, stream)
-                 : launch_walk_tn<T, KP, 1, GRAD>(a, keys, records, kept, stream);
+  if constexpr (kWalkOf<T, KP, GRAD>(2))
+    if (tn == 2) return launch_walk_tn<T, KP, 2, GRAD>(a, keys, records, kept, stream);
+  return launch_walk_tn<T, KP, 1, GRAD>(a, keys, records, kept, stream);
 }
 
 }  // namespace gdr

@@ -246,6 +246,32 @@ def test_many_heads(shape):
     assert torch.equal(o.t, o2) and torch.equal(S.t, S2)
 
 
+@pytest.mark.parametrize("dtype,shape", [  # B, HK, H, T, K, V: one, two and four tiles of values a block
+    ("bf16", (1, 12, 24, 150, 128, 128)), ("bf16", (4, 12, 12, 150, 72, 128)), ("bf16", (2, 20, 40, 150, 64, 64)),
+    ("f32", (2, 16, 16, 150, 128, 128)), ("f32", (3, 8, 16, 150, 64, 64)), ("f32", (1, 2, 2, 200, 128, 72)),
+])
+def test_tiles_a_block(dtype, shape):
+    inp = inputs.gdr_inputs(*shape, dtype, seed=sum(shape))
+    t = to_dev(inp, dtype)
+    o, S = mlstm.gdr_fwd(*(t[n] for n in ("q", "k", "v", "g", "beta", "S0")), mode="chunk")
+    o_ref, S_ref = oracle.gdr_sequential(*(inp[n] for n in ("q", "k", "v", "g", "beta", "S0")))
+    close(o, o_ref, dtype, coarse(inp, dtype, "chunk"))
+    close(S, S_ref, "f32")
+
+
+def test_four_tiles_a_block_packed():
+    lengths, T, H = (70, 0, 1, 64, 130, 5, 3, 128, 65, 12), 480, 14
+    inp = inputs.gdr_inputs(1, 7, H, T, 72, 128, "bf16", seed=8)
+    inp["S0"] = (0.1 * np.random.default_rng(8).standard_normal((10, H, 72, 128))).astype(np.float32)
+    o_ref, S_ref, off, terms = packed(inp, lengths)
+    t = to_dev(inp, "bf16")
+    o, S = mlstm.gdr_fwd(*(t[n] for n in ("q", "k", "v", "g", "beta", "S0")), seq_offsets=off)
+    used = sum(lengths)
+    close(o[:, :, :used], o_ref[:, :, :used], "bf16", terms[:, :, :used])
+    close(S, S_ref, "f32")
+    assert bool((o[:, :, used:] == 0).all())
+
+
 def test_many_heads_packed_strided_and_extreme():
     """Unlike lengths, token-major views, full resets and values that are not finite, on the tcgen05 pass."""
     lengths, T, H = (70, 0, 1, 64, 130, 5), 273, 32

@@ -132,6 +132,15 @@ def test_many_heads_take_wider_blocks(dtype):
         check(call(inp, dtype), inp, dtype)
 
 
+@pytest.mark.parametrize("dtype,shape", [  # one, two and four tiles of values a block
+    ("bf16", (1, 16, 32, 140, 128, 128)), ("bf16", (1, 32, 32, 80, 72, 256)), ("bf16", (3, 16, 32, 140, 64, 64)),
+    ("bf16", (2, 37, 37, 66, 32, 64)), ("f32", (2, 16, 16, 140, 128, 128)), ("f32", (3, 8, 16, 140, 64, 64)),
+])
+def test_tiles_a_block(dtype, shape):
+    inp = make(shape, dtype, 7)
+    check(call(inp, dtype), inp, dtype)
+
+
 def test_many_heads_packed():
     lengths, T = (70, 0, 1, 64, 130, 5), 273
     inp = make((1, 4, 8, T, 64, 48), "bf16", 6, True, len(lengths))
