@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kPrepThreads, ONE && sizeof(T) == 2 ? 4 : 3) g
 #pragma unroll
         for (int j = 0; j < KP / 32; ++j) {
           const int col = (j * 4 + part) * 8;
-          load8<T>(source(which) + col, row < len && col < a.K, x[j]);
+          load8(source(which) + col, row < len && col < a.K, x[j]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[j][e]));
         }

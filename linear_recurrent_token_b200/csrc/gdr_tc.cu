@@ -83,8 +83,6 @@ __device__ __forceinline__ void split_words(const float* x, float f, float (&hi)
     hi[j] = __uint_as_float(h), lo[j] = __uint_as_float(l);
   }
 }
-__device__ __forceinline__ void st_words(uint32_t at, const float (&w)[16]) { tmem_st16(at, w); }
-
 template <int KP>
 __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, const char* keys, const char* records,
                                                                unsigned int* err, long long limit) {
@@ -258,8 +256,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
       for (int i = 0; i < KH; i += 32) {
         float hi[16], lo[16];
         split_words(S + i, ss.mul, hi, lo);
-        st_words(ln + kTmS + (k0 + i) / 2, hi);
-        st_words(ln + kTmS + KP / 2 + (k0 + i) / 2, lo);
+        tmem_st16(ln + kTmS + (k0 + i) / 2, hi);
+        tmem_st16(ln + kTmS + KP / 2 + (k0 + i) / 2, lo);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -298,8 +296,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
       {
         float hi[TH / 2], lo[TH / 2];
         split_words(u, sz.mul, hi, lo);
-        st_words(ln + kTmZ + t0 / 2, hi);
-        st_words(ln + kTmZ + 32 + t0 / 2, lo);
+        tmem_st16(ln + kTmZ + t0 / 2, hi);
+        tmem_st16(ln + kTmZ + 32 + t0 / 2, lo);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -329,10 +327,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
       {
         float hi[TH / 2], lo[TH / 2];
         split_words(u, su.mul, hi, lo);
-        st_words(ln + kTmU + t0 / 2, hi);
+        tmem_st16(ln + kTmU + t0 / 2, hi);
         split_words(z, sw.mul, hi, lo);
-        st_words(ln + kTmZ + t0 / 2, hi);
-        st_words(ln + kTmZ + 32 + t0 / 2, lo);
+        tmem_st16(ln + kTmZ + t0 / 2, hi);
+        tmem_st16(ln + kTmZ + 32 + t0 / 2, lo);
       }
       const float keep = fac[kGam * kL + kL - 1 - t0];
       tmem_wait_st();

@@ -226,24 +226,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 8 consecutive elements as fp32, zeros where !in
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool in, float (&x)[8]) {
-  if (!in) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = unpack_bf16(u[e]);
-      x[2 * e] = f.x, x[2 * e + 1] = f.y;
-    }
-  } else {
-    const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-  }
+// 8 consecutive elements, zeros where !in
+__device__ __forceinline__ void load8(const float* p, bool in, float (&x)[8]) {
+  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 u = in ? *reinterpret_cast<const float4*>(p) : none, v = in ? *reinterpret_cast<const float4*>(p + 4) : none;
+  x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
 }
 
 // x, y (already scaled) as two fp16 parts

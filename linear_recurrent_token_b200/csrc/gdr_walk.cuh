@@ -77,7 +77,8 @@ struct Stage {
 
 // Warps that only copy.  With one or two tiles a block a scheduler has one or two warps that compute, and
 // copies of theirs (some 30 instructions a thread and chunk) would lengthen the chain; with four, registers
-// leave no room for more warps and the others hide them.
+// leave no room for more warps and the others hide them.  16 heads of 128 x 128, 8192 tokens, TN = 1: 283 us
+// without them, 266 with, 219 with R and P a chunk ahead as well.
 template <int TN>
 constexpr int kCopyWarps = TN == 1 ? 4 : TN == 2 ? 2 : 0;
 template <int TN>
