@@ -251,16 +251,16 @@ __global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads, TPR > kThread
     float v[NV][VEC], s[1] = {0.f};
     ring.wait();
     // Read from memory, a row's loads all come before the first store, which may lie on one of them (bf16 with
-    // residual, 33520 x 1001: 245 us, 316 vector by vector; 8186 x 4099: 170/517); read from shared memory,
-    // vector by vector, which takes fewer registers.
+    // residual, 33520 x 1001: 74 us, 316 vector by vector; 8186 x 4099: 146/517; four blocks an SM: 109, 144); read
+    // from shared memory, vector by vector, which takes fewer registers.
     constexpr int AHEAD = R::direct ? NV : 1;
     float add[AHEAD][VEC];
     if constexpr (R::direct) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        ring.read(turn, row, 0, i, v[i]);
-        if (res) ring.read(turn, row, 1, i, add[i]);
-      }
+      for (int i = 0; i < NV; ++i) ring.read(turn, row, 0, i, v[i]);
+      if (res)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) ring.read(turn, row, 1, i, add[i]);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads, TPR > kThread
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int c = i * TPR + t;  // a warp's 32 channels lie in one group (33520 x 1001: 1136 -> 397 us)
+          const int c = i * TPR + t;  // a warp's 32 channels lie in one group (33520 x 1001: an atomic a lane 1136 us, a warp 341)
           const uint32_t most = __reduce_max_sync(0xffffffffu, live && c < D ? m[i] : 0u);
           if ((t & 31) == 0 && c < D) atomicMax(&gmax[turn & 1][c / 128], most);  // the order does not matter
         }
