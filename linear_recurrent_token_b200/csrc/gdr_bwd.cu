@@ -220,21 +220,20 @@ struct GradStage {
   // dP o D by k's and q's scales and dW o D by k's, rows and columns, take the place of a head's last columns
   static constexpr int mats = 4 * NP * kTile;
   static constexpr int block = ds + NP * kVB * KP * 2 > mats ? ds + NP * kVB * KP * 2 : mats;
-  // factors and the operands' scales [5][4 tiles][4], twice; the scales in work as powers of two at most 1, and
-  // their largest
-  static constexpr int small = 2 * kFactorBytes + 3 * 5 * 16 * 4 + 8 * 4 + kGradThreads / 32 * 4 * 4;
+  // factors and the operands' scales [5][4 tiles][4], twice; the matrices' largest values [4][4 warps][64], then
+  // their scales [4][64] in the place of the first warp's
+  static constexpr int small = 2 * kFactorBytes + 2 * 5 * 16 * 4 + 4 * 4 * kL * 4;
   static constexpr int blocks = cols + 2 * block + small <= 227 * 1024 ? 2 : 1;
   static constexpr int bytes = cols + blocks * block + small;
   static_assert(bytes <= 227 * 1024, "a block's shared memory");
 };
 
-// acc[j] += f A B over one k step: A fragments (16 rows from r0) of a tile [k][row] (K_ROWS) or [row][k] with AC
-// columns, B of a tile [k][n] with BC columns from c0.  f, a power of two at most 1, scales A.  Two parts
-// each where NP is 2 (planes pa and pb bytes further on).
+// acc[j] += A B (or = A B where FRESH) over one k step: A fragments (16 rows from r0) of a tile [k][row] (K_ROWS)
+// or [row][k] with AC columns, B of a tile [k][n] with BC columns from c0.  Two parts each where NP is 2 (planes
+// pa and pb bytes further on).
 template <bool FRESH, bool K_ROWS, int AC, int BC, int NP, int NT>
 __device__ __forceinline__ void grad_step(float (&acc)[NT][4], uint32_t at, int pa, int r0, uint32_t bt, int pb, int c0, int kk,
-                                          float f, int lane) {
-  const __half2 f2 = __float2half2_rn(f);
+                                          int lane) {
   uint4 a[2];
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
@@ -243,17 +242,16 @@ __device__ __forceinline__ void grad_step(float (&acc)[NT][4], uint32_t at, int 
       ldsm4t(r, at + p * pa + piece_at<AC>(kk * 16 + at_row(lane), r0 + at_col(lane)));
     else
       ldsm4(r, at + p * pa + piece_at<AC>(r0 + bt_row(lane), kk * 16 + bt_col(lane)));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&r[i]), f2);
-      r[i] = *reinterpret_cast<const uint32_t*>(&x);
-    }
     a[p] = make_uint4(r[0], r[1], r[2], r[3]);
   }
   step<FRESH, NT, NP, NP>(acc, a[0], a[NP - 1], [&](uint32_t (&r)[4], int j, int plane) {
     ldsm4t(r, bt + plane * pb + piece_at<BC>(kk * 16 + bt_row(lane), c0 + j * 8 + bt_col(lane)));
   });
 }
+template <int N>
+struct Columns {
+  static constexpr int value = N;
+};
 // sum += acc times a factor of the row (the lane's rows r and r + 8)
 template <int NT>
 __device__ __forceinline__ void add_rows(float (&sum)[NT][4], const float (&acc)[NT][4], float f0, float f1) {
@@ -266,9 +264,8 @@ __device__ __forceinline__ void add_rows(float (&sum)[NT][4], const float (&acc)
 // One block for each chunk and key head; the value heads that share it follow one another and their
 // shares add up in registers.  Warp (t, n) of 4 x 4 has 16 tokens and a quarter of the keys (or of the other
 // token).  The kept operands come 64 value columns at a time, the next ones while these are in work.
-// 2048 chunks of 128 x 128: 171 us, issue slots 41 % taken, tensor pipes 23 %: reading and scaling the operands'
-// fragments, and the barriers of a block that has its SM alone.  (Blocks that stay and fetch the next
-// chunk meanwhile took 178 us: registers ran out.)
+// 2048 chunks of 128 x 128: 177 us.  What bounds it is reading the operands' fragments, and the barriers of a block
+// that has its SM alone.  (Blocks that stay and fetch the next chunk meanwhile took 7 us more: registers ran out.)
 template <typename T, int KP>
 __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a, const char* keys, const char* records,
                                                                 const Kept kept) {
@@ -277,9 +274,7 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
   extern __shared__ __align__(128) char smem[];
   float* const factors = reinterpret_cast<float*>(smem + L::cols + L::blocks * L::block);  // [2][kFactors][64]
   float* const scales = factors + 2 * kFactors * kL;                                       // [2][operand][tile][quarter]
-  float* rel = scales + 2 * 5 * 16;  // [operand][tile][quarter]
-  float* top = rel + 5 * 16;
-  float* most = top + 8;  // [16 warps][4]
+  float* const most = scales + 2 * 5 * 16;  // [matrix][warp][64], then [matrix][64]
   int n, c;
   Seq s;
   if (!find_chunk(a, blockIdx.x, &n, &s, &c)) return;
@@ -340,111 +335,122 @@ __global__ void __launch_bounds__(kGradThreads) gdr_grad_kernel(const GdrArgs a,
     if (L::blocks == 2 && i + 1 < total) fetch(i + 1);
     const float* fac = factors + (i / parts & 1) * kFactors * kL;
     if (part == 0) zero(dP), zero(dW);
-    if (tid < 5 * 32) {  // a warp an operand: its 16 scales against their largest
-      const float x = lane < 16 ? scales[((i & 1) * 5 + warp) * 16 + lane] : 0.f;
-      const float big = warp_max(x);
-      if (lane < 16) rel[warp * 16 + lane] = big > 0.f ? x / big : 0.f;
-      if (lane == 0) top[warp] = big;
-    }
-    __syncthreads();
     const uint32_t st = su + L::cols + (L::blocks == 2 ? (i & 1) * L::block : 0);
     constexpr int ps = kVB * KP * 2;
-    const float *ro = rel, *rv = rel + 16, *ru = rel + 32, *rs = rel + 48, *rd = rel + 64;
-    float acc[NT][4], p[2][4];
-#define MLSTM_GRAD_OVER_VALUES(ACC, K_ROWS, BC, A, RA, B, PB, C0, RB)                                              \
-  grad_step<true, K_ROWS, kL, BC, NP>(ACC, st + A, kTile, r0, st + B, PB, C0, 0, RA[mt] * RB[nq], lane);           \
-  _Pragma("unroll") for (int kk = 1; kk < 4; ++kk) grad_step<false, K_ROWS, kL, BC, NP>(                           \
-      ACC, st + A, kTile, r0, st + B, PB, C0, kk, RA[kk * 4 + mt] * RB[kk * 4 + nq], lane)
-    MLSTM_GRAD_OVER_VALUES(acc, true, KP, L::dout, ro, L::s, ps, k0, rs);  // gam (dO S^T)
-    {
-      const float f = top[0] * top[3];
-      add_rows(dq, acc, fac[kGam * kL + ra] * f, fac[kGam * kL + ra + 8] * f);
-    }
-    MLSTM_GRAD_OVER_VALUES(acc, true, KP, L::dv, rv, L::s, ps, k0, rs);  // -gam (dV S^T)
-    {
-      const float f = -top[1] * top[3];
-      add_rows(dk, acc, fac[kGam * kL + ra] * f, fac[kGam * kL + ra + 8] * f);
-    }
-    MLSTM_GRAD_OVER_VALUES(acc, true, KP, L::u, ru, L::ds, ps, k0, rd);  // w (U dS^T)
-    {
-      const float f = top[2] * top[4];
-      add_rows(dk, acc, fac[kW * kL + ra] * f, fac[kW * kL + ra + 8] * f);
-    }
+    const float* sc = scales + (i & 1) * 5 * 16;
+    const float *so = sc, *sv = sc + 16, *su_ = sc + 32, *ss = sc + 48, *sd = sc + 64;
+    // Every tile of 16 columns is a product from zero, scaled on its way into the fp32 sum: the scales of dO, S and
+    // the others may lie any powers apart from tile to tile.  (Fragments that were scaled to share one sum took
+    // 171 us and lost what lay 2^-25 below the largest product of two scales.)  f0, f1: further factors of the
+    // rows.  Two tiles in flight with 128 keys, which have twice the sums (four: spills, 192 us; one: 182).
+    auto over_values = [&](auto& sum, auto bc, int A, const float* fa, int B, int pb, int c0, const float* fb, float f0,
+                           float f1) {
+#pragma unroll(KP == 128 ? 2 : 4)
+      for (int kk = 0; kk < 4; ++kk) {
+        float acc[sizeof(sum) / sizeof(sum[0])][4];
+        grad_step<true, true, kL, decltype(bc)::value, NP>(acc, st + A, kTile, r0, st + B, pb, c0, kk, lane);
+        const float f = fminf(fa[kk * 4 + mt] * fb[kk * 4 + nq], 0x1p127f);  // (a zero times infinity is none)
+        add_rows(sum, acc, f * f0, f * f1);
+      }
+    };
+    const Columns<KP> by_key;
+    const Columns<kL> by_token;
+    const float g0 = fac[kGam * kL + ra], g1 = fac[kGam * kL + ra + 8];
+    over_values(dq, by_key, L::dout, so, L::s, ps, k0, ss, g0, g1);                                     // gam (dO S^T)
+    over_values(dk, by_key, L::dv, sv, L::s, ps, k0, ss, -g0, -g1);                                     // -gam (dV S^T)
+    over_values(dk, by_key, L::u, su_, L::ds, ps, k0, sd, fac[kW * kL + ra], fac[kW * kL + ra + 8]);  // w (U dS^T)
     if (c0 <= r0) {  // the other token's quarter is not behind this one
-      MLSTM_GRAD_OVER_VALUES(p, true, kL, L::dout, ro, L::u, kTile, c0, ru);
-      add_scaled(dP, p, top[0] * top[2]);
-      MLSTM_GRAD_OVER_VALUES(p, true, kL, L::dv, rv, L::u, kTile, c0, ru);
-      add_scaled(dW, p, top[1] * top[2]);
+      over_values(dP, by_token, L::dout, so, L::u, kTile, c0, su_, 1.f, 1.f);
+      over_values(dW, by_token, L::dv, sv, L::u, kTile, c0, su_, 1.f, 1.f);
     }
-#undef MLSTM_GRAD_OVER_VALUES
     if (part == parts - 1) {
-      // (dP o D), (dW o D) with the scales of the rows that they meet, one power of two a matrix
-      float big[4] = {0.f, 0.f, 0.f, 0.f};
+      // (dP o D), (dW o D) with the scales of the rows that they meet; each row of the four products has a power of
+      // two of its own: 0, 2 are read by rows (tokens), 1, 3 by columns
+      float row[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, column[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
       const float2* G = reinterpret_cast<const float2*>(fac + kG * kL);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int t = ra + (e >> 1) * 8, q = c0 + j * 8 + ca + (e & 1);
+          const int t = ra + (e >> 1) * 8, q = c0 + j * 8 + ca + (e & 1), at = 2 * j + (e & 1);
           const float D = q <= t ? decay_between(G[t], G[q]) : 0.f;
           dP[j][e] = q <= t ? dP[j][e] * D : 0.f;
           dW[j][e] = q < t ? dW[j][e] * D : 0.f;
-          big[0] = fmaxf(big[0], fabsf(dP[j][e] * fac[kKInv * kL + q]));
-          big[1] = fmaxf(big[1], fabsf(dP[j][e] * fac[kQInv * kL + t]));
-          big[2] = fmaxf(big[2], fabsf(dW[j][e] * fac[kKInv * kL + q]));
-          big[3] = fmaxf(big[3], fabsf(dW[j][e] * fac[kKInv * kL + t]));
+          row[0][e >> 1] = fmaxf(row[0][e >> 1], fabsf(dP[j][e] * fac[kKInv * kL + q]));
+          column[0][at] = fmaxf(column[0][at], fabsf(dP[j][e] * fac[kQInv * kL + t]));
+          row[1][e >> 1] = fmaxf(row[1][e >> 1], fabsf(dW[j][e] * fac[kKInv * kL + q]));
+          column[1][at] = fmaxf(column[1][at], fabsf(dW[j][e] * fac[kKInv * kL + t]));
         }
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        big[m] = warp_max(big[m]);
-        if (lane == 0) most[warp * 4 + m] = big[m];
+      for (int m = 0; m < 2; ++m) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          for (int d = 1; d < 4; d *= 2) row[m][x] = fmaxf(row[m][x], __shfl_xor_sync(0xffffffffu, row[m][x], d));
+          if ((lane & 3) == 0) most[(2 * m * 4 + nq) * kL + ra + 8 * x] = row[m][x];
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          for (int d = 4; d < 32; d *= 2) column[m][x] = fmaxf(column[m][x], __shfl_xor_sync(0xffffffffu, column[m][x], d));
+          if (lane < 4) most[((2 * m + 1) * 4 + mt) * kL + c0 + (x >> 1) * 8 + ca + (x & 1)] = column[m][x];
+        }
       }
       __syncthreads();  // the columns are read; the matrices take their place
-      Scale sc[4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) sc[m] = scale_of(warp_max(lane < 16 ? most[lane * 4 + m] : 0.f));
+      if (tid < 4 * kL) {
+        float* at = most + (tid / kL * 4) * kL + tid % kL;
+        *at = scale_of(fmaxf(fmaxf(at[0], at[kL]), fmaxf(at[2 * kL], at[3 * kL]))).inv;
+      }
+      __syncthreads();
+      // the inverses, and the powers themselves
+      auto inv = [&](int m, int x) { return most[m * 4 * kL + x]; };
+      auto mul = [&](int m, int x) { return __uint_as_float((254u << 23) - __float_as_uint(inv(m, x))); };
       char* mats = smem + (st - su);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int r = 0; r < 2; ++r) {
+        const int t = ra + r * 8;
+        const float kt = fac[kKInv * kL + t], qt = fac[kQInv * kL + t], m0 = mul(0, t), m2 = mul(2, t);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int t = ra + r * 8, q = c0 + j * 8 + ca;
+        for (int j = 0; j < 2; ++j) {
+          const int q = c0 + j * 8 + ca;
           const float2 ki = *reinterpret_cast<const float2*>(fac + kKInv * kL + q);
-          const float kt = fac[kKInv * kL + t], qt = fac[kQInv * kL + t];
           const float x = dP[j][2 * r], y = dP[j][2 * r + 1], z = dW[j][2 * r], w = dW[j][2 * r + 1];
-          const float v[4][2] = {{x * ki.x, y * ki.y}, {x * qt, y * qt}, {z * ki.x, w * ki.y}, {z * kt, w * kt}};
+          const float v[4][2] = {{x * ki.x * m0, y * ki.y * m0},
+                                 {x * qt * mul(1, q), y * qt * mul(1, q + 1)},
+                                 {z * ki.x * m2, w * ki.y * m2},
+                                 {z * kt * mul(3, q), w * kt * mul(3, q + 1)}};
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             uint32_t hi, lo;
-            split(v[m][0] * sc[m].mul, v[m][1] * sc[m].mul, hi, lo);
+            split(v[m][0], v[m][1], hi, lo);
             char* at = mats + m * NP * kTile + piece_at<kL>(t, q) + (q & 7) * 2;
             *reinterpret_cast<uint32_t*>(at) = hi;
             if (NP == 2) *reinterpret_cast<uint32_t*>(at + kTile) = lo;
           }
         }
+      }
       __syncthreads();
       const uint32_t ku = su, qu = su + keys_bytes(KP, NP) / 2;
       constexpr int pk = kL * KP * 2, mat = NP * kTile;
+      float acc[NT][4];
       zero(acc);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        if (kk <= mt) grad_step<false, false, kL, KP, NP>(acc, st, kTile, r0, ku, pk, k0, kk, 1.f, lane);
-      add_scaled(dq, acc, sc[0].inv);
+        if (kk <= mt) grad_step<false, false, kL, KP, NP>(acc, st, kTile, r0, ku, pk, k0, kk, lane);
+      add_rows(dq, acc, inv(0, ra), inv(0, ra + 8));
       zero(acc);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        if (kk >= mt) grad_step<false, true, kL, KP, NP>(acc, st + mat, kTile, r0, qu, pk, k0, kk, 1.f, lane);
-      add_scaled(dk, acc, sc[1].inv);
+        if (kk >= mt) grad_step<false, true, kL, KP, NP>(acc, st + mat, kTile, r0, qu, pk, k0, kk, lane);
+      add_rows(dk, acc, inv(1, ra), inv(1, ra + 8));
       zero(acc);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        if (kk <= mt) grad_step<false, false, kL, KP, NP>(acc, st + 2 * mat, kTile, r0, ku, pk, k0, kk, 1.f, lane);
-      add_scaled(dk, acc, -sc[2].inv);
+        if (kk <= mt) grad_step<false, false, kL, KP, NP>(acc, st + 2 * mat, kTile, r0, ku, pk, k0, kk, lane);
+      add_rows(dk, acc, -inv(2, ra), -inv(2, ra + 8));
       zero(acc);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        if (kk >= mt) grad_step<false, true, kL, KP, NP>(acc, st + 3 * mat, kTile, r0, ku, pk, k0, kk, 1.f, lane);
-      add_scaled(dk, acc, -sc[3].inv);
+        if (kk >= mt) grad_step<false, true, kL, KP, NP>(acc, st + 3 * mat, kTile, r0, ku, pk, k0, kk, lane);
+      add_rows(dk, acc, -inv(3, ra), -inv(3, ra + 8));
     }
     if (L::blocks == 1 && i + 1 < total) {
       __syncthreads();
