@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
     char *st = smem + L::at(c), *mats = smem + L::mats(c);
     const float* fac = reinterpret_cast<const float*>(st + L::factors);
     {
-      const Scale sc = scale_of(tile_max(D));
+      const Scale sc = tile_scale(D);
       give<KS, 2>(D, sc, ex + L::fs, inv, w, lane);
       if (live) {  // dS for the gradients of k, and <dS, S> with the state that the forward pass left here
         const size_t after = ((size_t)(rec + n + 1) * a.H + h) * tiles + tile;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
     {
       float d[2][4];
       read_columns<T, L::row>(d, st + L::dout + w * 16 * L::row + local * 16 * (int)sizeof(T), lane);
-      if (live) keep_tokens<NK>(kept.dO, kept.dO_inv, base, d, scale_of(tile_max(d)), w, lane);
+      if (live) keep_tokens<NK>(kept.dO, kept.dO_inv, base, d, tile_scale(d), w, lane);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float2 pi = factor(fac + kPInv * kL, w * 16, j, lane), gq = factor(fac + kGQ * kL, w * 16, j, lane);
@@ -114,8 +114,8 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
           y[j][e] = d[j][e] * (e & 1 ? gq.y : gq.x);
         }
       }
-      give<1, NP>(x, scale_of(tile_max(x)), ex + L::fu, inv + 2 * kQuarter, w, lane);
-      give<1, 2>(y, scale_of(tile_max(y)), ex + L::fz, inv + 4 * kQuarter, w, lane);
+      give<1, NP>(x, tile_scale(x), ex + L::fu, inv + 2 * kQuarter, w, lane);
+      give<1, 2>(y, tile_scale(y), ex + L::fz, inv + 4 * kQuarter, w, lane);
     }
     // dU = w (K dS) + P^T dO
     by_keys<KP, NP, false, false>(x, y, ex + L::fs, inv, smem_u32(st), 0u, w, lane);
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
         y[j][e] = x[j][e] * (e & 1 ? be.y * ri.y : be.x * ri.x);
       }
     }
-    give<1, 2>(y, scale_of(tile_max(y)), ex + fy, inv + kQuarter, w, lane);
+    give<1, 2>(y, tile_scale(y), ex + fy, inv + kQuarter, w, lane);
     tile_barrier(local);  // beta dU is in exchange
     // dY = dU + R^T (beta dU), dV = beta dY
     by_tokens<true, 2, 2>(y, ex + fy, inv + kQuarter, smem_u32(mats), w, lane);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
           y[j][e] = x[j][e] * (e & 1 ? -gk.y : -gk.x);
         }
       }
-      give<1, 2>(y, scale_of(tile_max(y)), ex + L::fw, inv + 3 * kQuarter, w, lane);
+      give<1, 2>(y, tile_scale(y), ex + L::fw, inv + 3 * kQuarter, w, lane);
       const float2 db = column_sum(dot, lane);
       read_columns<T, L::row>(v, vt, lane);
 #pragma unroll
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
           const float2 was = *reinterpret_cast<const float2*>(kept.dots + at);
           *reinterpret_cast<float2*>(kept.dots + at) = make_float2(was.x - dv.x, was.y - dv.y);
         }
-        keep_tokens<NK>(kept.dV, kept.dV_inv, base, x, scale_of(tile_max(x)), w, lane);
+        keep_tokens<NK>(kept.dV, kept.dV_inv, base, x, tile_scale(x), w, lane);
       }
     }
     tile_barrier(local);  // gam dV is in exchange

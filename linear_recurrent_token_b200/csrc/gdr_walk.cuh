@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
     char *st = smem + L::at(c), *mats = smem + L::mats(c);
     const float* fac = reinterpret_cast<const float*>(st + L::factors);
     {
-      const Scale sc = scale_of(tile_max(S));
+      const Scale sc = tile_scale(S);
       give<KS, 2>(S, sc, ex + L::fs, inv, w, lane);
       keep_state(rec + n, sc);
     }
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
         u[j][e] = (e & 1 ? be.y : be.x) * z[j][e];
       }
     }
-    give<1, 2>(u, scale_of(tile_max(u)), ex + L::fz, inv + kQuarter, w, lane);
+    give<1, 2>(u, tile_scale(u), ex + L::fz, inv + kQuarter, w, lane);
     if (copies && !L::ahead) cp_wait<L::chunks == 2 ? 1 : 0>();
     if (L::ahead)
       tile_barrier(local);  // beta Z is in exchange
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
       }
     }
     {
-      const Scale sc = scale_of(tile_max(u));
+      const Scale sc = tile_scale(u);
       give<1, L::nu>(u, sc, ex + L::fu, inv + 2 * kQuarter, w, lane);
       if constexpr (GRAD) {
         if (live) {
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
         }
       }
     }
-    give<1, 2>(uw, scale_of(tile_max(uw)), ex + L::fw, inv + 3 * kQuarter, w, lane);
+    give<1, 2>(uw, tile_scale(uw), ex + L::fw, inv + 3 * kQuarter, w, lane);
     tile_barrier(local);  // U and w U are in exchange
     // O += P U
     by_tokens<false, L::nu, L::nu>(x, ex + L::fu, inv + 2 * kQuarter, smem_u32(mats) + 2 * kTile, w, lane);
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
       if (copies) fetch_all<T, KP, TN, GRAD>(a, s, c + 1, h, col0, keys, records, smem_u32(smem));
     }
   }
-  if constexpr (GRAD) keep_state(s.slot + chunks + n, scale_of(tile_max(S)));
+  if constexpr (GRAD) keep_state(s.slot + chunks + n, tile_scale(S));
   if (a.S_out) {
 #pragma unroll
     for (int j = 0; j < 2 * KS; ++j)

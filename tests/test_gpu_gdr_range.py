@@ -1,8 +1,12 @@
-"""The gated delta rule where magnitudes differ within a call: gradients far below their neighbours'."""
+"""The gated delta rule where magnitudes differ within a call: gradients far below their neighbours', and
+columns with an infinity beside others without."""
 import numpy as np
 import pytest
+import torch
 
 import oracle
+from linear_recurrent_token_b200 import inputs, mlstm
+from tests.test_gpu_gdr import to_dev
 from tests.test_gpu_gdr_backward import COARSE, HALF, NAMES, call, magnitudes, make
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +81,67 @@ def test_small_rows_among_the_products_of_tokens(dtype, shape):
     out, ref, mag = both(inp, dtype)
     held_by_row(out["dq"], ref["dq"], mag["dq"], dtype)
     held_by_row(out["dk"], ref["dk"], mag["dk"], dtype)
+
+
+# One, two and four tiles of values a block in both types, and the tcgen05 pass: B, HK, H, T, K, V
+FORWARD = [
+    ("bf16", (1, 2, 4, 150, 64, 48)), ("bf16", (1, 1, 2, 150, 128, 72)), ("bf16", (1, 12, 24, 150, 128, 128)),
+    ("bf16", (4, 12, 12, 150, 72, 128)), ("bf16", (2, 20, 40, 150, 64, 64)), ("bf16", (20, 2, 4, 130, 128, 128)),
+    ("f32", (1, 2, 2, 150, 64, 48)), ("f32", (1, 2, 2, 200, 128, 72)), ("f32", (2, 16, 16, 150, 128, 128)),
+    ("f32", (3, 8, 16, 150, 64, 64)),
+]
+BACKWARD = [
+    ("bf16", (1, 2, 4, 140, 64, 48)), ("bf16", (1, 1, 2, 140, 128, 72)), ("bf16", (1, 16, 32, 140, 128, 128)),
+    ("bf16", (1, 32, 32, 100, 72, 256)), ("bf16", (3, 16, 32, 140, 64, 64)), ("bf16", (2, 37, 37, 100, 32, 64)),
+    ("f32", (1, 2, 2, 140, 64, 48)), ("f32", (2, 16, 16, 140, 128, 128)), ("f32", (3, 8, 16, 140, 64, 64)),
+]
+COLUMN, TOKEN, BEFORE = 3, 85, 80  # the infinity's, and the first token of its group of 16
+
+
+def without_column(V):
+    return [c for c in range(V) if c != COLUMN]
+
+
+@pytest.mark.parametrize("name", ["v", "S0"])
+@pytest.mark.parametrize("mode", ["chunk", "recurrent"])
+@pytest.mark.parametrize("dtype,shape", FORWARD)
+def test_an_infinity_stays_in_its_column(dtype, shape, mode, name):
+    """Bitwise: the column is 2^-20 of the others, so no scale is its own with or without the infinity."""
+    inp = inputs.gdr_inputs(*shape, dtype, seed=71)
+    inp["v"][..., COLUMN] *= 2.0 ** -20
+    inp["S0"][..., COLUMN] *= 2.0 ** -20
+    t = to_dev(inp, dtype)
+    run = lambda: mlstm.gdr_fwd(*(t[n] for n in ("q", "k", "v", "g", "beta", "S0")), mode=mode)
+    o, S = run()
+    if name == "v":
+        t["v"][:, :, TOKEN, COLUMN] = float("inf")
+    else:
+        t["S0"][:, :, 5, COLUMN] = -float("inf")
+    o2, S2 = run()
+    rest = without_column(shape[-1])
+    assert torch.equal(o[..., rest], o2[..., rest]) and torch.equal(S[..., rest], S2[..., rest])
+    first = TOKEN if name == "v" else 0
+    assert not bool(torch.isfinite(o2[:, :, first:, COLUMN]).any()) and not bool(torch.isfinite(S2[..., COLUMN]).any())
+    if name == "v":  # nor does it reach the chunk before
+        assert torch.equal(o[:, :, :64], o2[:, :, :64])
+
+
+@pytest.mark.parametrize("name", ["v", "S0", "do", "dS"])
+@pytest.mark.parametrize("dtype,shape", BACKWARD)
+def test_an_infinity_stays_in_its_column_of_the_gradients(dtype, shape, name):
+    inp = make(shape, dtype, 72)
+    for n in ("v", "S0", "do", "dS"):
+        inp[n][..., COLUMN] *= 2.0 ** -20
+    a = call(inp, dtype)
+    if name in ("v", "do"):
+        inp[name][:, :, TOKEN, COLUMN] = np.inf
+    else:
+        inp[name][:, :, 5, COLUMN] = np.inf
+    b = call(inp, dtype)
+    rest = without_column(shape[-1])
+    assert all(torch.equal(a[n][..., rest], b[n][..., rest]) for n in ("dv", "dS0"))
+    if name in ("do", "dS"):  # (dv, dS0 are linear in these two; what v and S0 reach is dq, dk and the gates)
+        assert not bool(torch.isfinite(b["dv"][:, :, :TOKEN, COLUMN]).any())
+    if name == "v":  # a token's dq depends on tokens up to it
+        assert torch.equal(a["dq"][:, :, :BEFORE], b["dq"][:, :, :BEFORE])
+        assert not bool(torch.isfinite(b["dq"][:, :, TOKEN:]).any())
