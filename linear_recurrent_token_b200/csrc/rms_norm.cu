@@ -343,8 +343,9 @@ __global__ void __launch_bounds__(TPR > kThreads ? TPR : kThreads, TPR > kThread
       for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + t) * VEC;
         const float amax = __uint_as_float(m[i]);
-        // one reciprocal for the group, from a maximum that is in its range
-        const float up = amax < 1e-30f ? 0x1p100f : 1.f, f = m[i] == 0 ? 0.f : __fdividef(kTop, amax * up);
+        // one quick division for the group (whose result is 0 above 2^126), of a maximum brought into its range
+        const float up = amax < 1e-30f ? 0x1p100f : amax > 0x1p100f ? 0x1p-100f : 1.f;
+        const float f = m[i] == 0 ? 0.f : __fdividef(kTop, amax * up);
         if (up != 1.f)
 #pragma unroll
           for (int e = 0; e < VEC; ++e) v[i][e] *= up;
