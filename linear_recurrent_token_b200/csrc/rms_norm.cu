@@ -524,11 +524,12 @@ template <typename T, int VEC, int TPR>
 cudaError_t bwd_rows(const RmsArgs& a, cudaStream_t stream) {
   constexpr int block = TPR > kThreads ? TPR : kThreads, rpb = block / TPR;
   const int grid = bwd_blocks(a.rows, rpb);
-  const size_t sums = rpb > 1 && a.dweight ? sizeof(float) * rpb * a.D : 0;  // at most 8 rows of 512
-  constexpr size_t ring = Ring<T, VEC, 3, TPR>::bytes;
-  const size_t smem = sums > ring ? sums : ring;
+  const int sums = rpb > 1 && a.dweight ? (int)sizeof(float) * rpb * a.D : 0;
+  constexpr int ring = Ring<T, VEC, 3, TPR>::bytes, most_sums = rpb > 1 ? (int)sizeof(float) * rpb * TPR * kElems : 0;
+  const int smem = sums > ring ? sums : ring;
   const auto kernel = rms_norm_bwd_kernel<T, VEC, TPR>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the same limit from every call: it belongs to the function, and another thread may set it before this launch
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ring > most_sums ? ring : most_sums);
   if (e != cudaSuccess) return e;
   kernel<<<grid, block, smem, stream>>>((const T*)a.dy, (const T*)a.x, a.weight, a.eps,
                                                                   (const T*)a.res, (T*)a.y,

@@ -1,4 +1,8 @@
-"""The root-mean-square norm at the ends of its range: outputs near fp32's largest."""
+"""The root-mean-square norm at the ends of its range: outputs near fp32's largest, calls of several threads at
+once."""
+import ctypes
+import threading
+
 import pytest
 import torch
 
@@ -28,3 +32,35 @@ def test_outputs_near_the_largest(dtype, quant, D, group, power):
         step = torch.clamp(want.abs() * 2.0 ** -4, min=2.0 ** -10) if quant == "e4m3" else torch.full_like(want, 0.5)
         assert bool(((got - want).abs() <= step + 2.0 ** -18 * want.abs()).all())
         assert bool((got.abs().amax(-1) == TOP[quant]).all())
+
+
+def test_threads_with_rows_of_other_widths():
+    """Four threads whose calls run the same kernel with other amounts of shared memory (widths 511 and 301 without
+    whole 16-byte accesses, with the weight's gradient and without): none is refused, results as alone."""
+    L, refused, wrong = mlstm.lib(), [], []
+
+    def work(D, want_dw):
+        stream = torch.cuda.Stream()
+        gen = torch.Generator(device="cuda").manual_seed(D)
+        r, dy = (torch.randn(8, D, generator=gen, device="cuda") for _ in range(2))
+        ref, ref_dw = mlstm.rms_norm_bwd(dy, r)
+        dx, dw = torch.empty_like(r), torch.empty(D, device="cuda")
+        p = mlstm.RmsParams(8, D, 0, 0, 0, 1e-6)
+        need = L.mlstm_rms_norm_bwd_workspace_size(ctypes.byref(p))
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        args = (ctypes.byref(p), dy.data_ptr(), r.data_ptr(), None, None, dx.data_ptr(), dw.data_ptr() if want_dw else None,
+                ws.data_ptr(), need, stream.cuda_stream)
+        for _ in range(20000):
+            if L.mlstm_rms_norm_bwd(*args) != 0:
+                refused.append((D, want_dw))
+        stream.synchronize()
+        if not torch.equal(dx, ref) or (want_dw and not torch.equal(dw, ref_dw)):
+            wrong.append((D, want_dw))
+
+    threads = [threading.Thread(target=work, args=a) for a in ((511, True), (301, False), (511, True), (301, True))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not refused and not wrong
