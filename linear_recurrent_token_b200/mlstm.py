@@ -594,6 +594,8 @@ def _on(device, stream, tensors, body):
     stream; the allocator is told of tensors that come from another one."""
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, got {device}")
+    if stream is not None and stream.device != device:  # its kernels would run there, on memory of this one
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     if stream is None and device.index == torch._C._cuda_getDevice():  # as torch.cuda.current_device, less wrapping
         return body(torch._C._cuda_getCurrentRawStream(device.index))
     with torch.cuda.device(device):
