@@ -673,7 +673,10 @@ def gdr_bwd_workspace_size(params: GdrParams) -> int:
 def gdr_status(params: GdrParams, workspace, *, stream=None) -> int:
     """Outcome of the bounded waits of the last gdr_fwd with these params and this workspace
     (mlstm_gdr_status; synchronises): 0 ok, 8 a wait ran out (MLSTM_ERR_TIMEOUT)."""
-    return int(lib().mlstm_gdr_status(ctypes.byref(params), _ptr(workspace), _stream_ptr(stream)))
+    if workspace is None:
+        return int(lib().mlstm_gdr_status(ctypes.byref(params), None, _stream_ptr(stream)))
+    return _on(workspace.device, stream, (),
+               lambda cs: int(lib().mlstm_gdr_status(ctypes.byref(params), workspace.data_ptr(), cs)))
 
 
 def _like(t, packed):
