@@ -1,11 +1,14 @@
 """The gated delta rule where magnitudes differ within a call: gradients far below their neighbours', and
 columns with an infinity beside others without."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import oracle
 from linear_recurrent_token_b200 import inputs, mlstm
+from tests.helpers import TORCH_DTYPE, Guarded, dev
 from tests.test_gpu_gdr import to_dev
 from tests.test_gpu_gdr_backward import COARSE, HALF, NAMES, call, magnitudes, make
 
@@ -145,3 +148,25 @@ def test_an_infinity_stays_in_its_column_of_the_gradients(dtype, shape, name):
     if name == "v":  # a token's dq depends on tokens up to it
         assert torch.equal(a["dq"][:, :, :BEFORE], b["dq"][:, :, :BEFORE])
         assert not bool(torch.isfinite(b["dq"][:, :, TOKEN:]).any())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [[-5, 40, 1000], [80, 10, 90], [2**31 - 1, -2**31, 5], [91, 92, 93], [0, 90, 0]])
+def test_gradients_with_offsets_out_of_order_stay_inside(dtype, bad):
+    """The C entry between guards: outputs, workspace, and inputs that must not change."""
+    B, HK, H, T, K, V = 1, 1, 2, 90, 32, 16
+    inp = make((B, HK, H, T, K, V), dtype, 2, True, 2)
+    td, f32 = TORCH_DTYPE[dtype], torch.float32
+    ins = [dev(inp[n], td) for n in ("q", "k", "v")] + [dev(inp[n]) for n in ("g", "beta", "S0")]
+    ins += [torch.tensor(bad, dtype=torch.int32, device="cuda"), dev(inp["do"], td), dev(inp["dS"])]
+    kept = [x.clone() for x in ins]
+    outs = [Guarded(s, d) for s, d in (((B, HK, T, K), td), ((B, HK, T, K), td), ((B, H, T, V), td), ((B, H, T), f32),
+                                       ((B, H, T), f32), ((2, H, K, V), f32))]
+    p = mlstm.gdr_params(*ins[:5], ins[7], seq_offsets=ins[6])
+    ws = Guarded((mlstm.gdr_bwd_workspace_size(p),), torch.uint8)
+    by = [mlstm.GdrStride(h * T * d, T * d, d) for h, d in ((HK, K), (HK, K), (H, V))]
+    st = mlstm.lib().mlstm_gdr_bwd(ctypes.byref(p), *(x.data_ptr() for x in ins), *by, *(x.t.data_ptr() for x in outs),
+                                   ws.t.data_ptr(), ws.t.numel(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and ws.intact() and all(x.intact() for x in outs)
+    assert all(torch.equal(x, y) for x, y in zip(ins, kept))
