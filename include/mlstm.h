@@ -481,7 +481,11 @@ mlstm_status_t mlstm_step(const mlstm_step_params_t* p,
  * the strides given here, in elements; the last axis of q, k, v, o is contiguous.  So a projection's
  * output [B,T,heads,width], or a slice of a wider one, is read where it lies.  Strides are >= 0 (0
  * repeats an input); those of q, k, v, o are multiples of 16 bytes, and distinct elements of an
- * output lie apart.  States are dense.
+ * output lie apart.  States are dense.  An output's memory from its first to its last element holds no
+ * element of an input or of another output (MLSTM_ERR_ALIAS), not even in the gaps between its rows.
+ *
+ * Sizes.  K and V multiples of 8, V at most 2^20; B, H and num_seqs at most 65535, T at most 2^30, B T at
+ * most 2^36.
  *
  * Packed sequences (num_seqs = N > 0).  B is 1 and sequence n is the tokens seq_offsets[n] ..
  * seq_offsets[n+1] - 1 of the T tokens: seq_offsets [N+1] int32 on the device, not decreasing, at most
@@ -492,10 +496,20 @@ mlstm_status_t mlstm_step(const mlstm_step_params_t* p,
  *
  *   p->mode  MLSTM_GDR_RECURRENT: token by token, fp32 arithmetic; K a multiple of 8, at most 256.
  *            MLSTM_GDR_CHUNK: chunks of 64 tokens on the tensor cores, a triangular solve per chunk;
- *            K a multiple of 8, at most 128.  Operands are split into 16-bit parts so that states and
- *            gate gradients keep fp32 accuracy.
+ *            K a multiple of 8, at most 128.
  *            MLSTM_GDR_AUTO: CHUNK from 32 tokens (T) on where K allows it (packed: and 8 a sequence on
  *            average), else RECURRENT.
+ *
+ * Accuracy in chunks.  Operands are split into 16-bit parts under powers of two.  States, and for fp32
+ * inputs outputs, have the errors of fp32 arithmetic, relative to the largest value nearby (16 value
+ * columns by 16 tokens or a quarter of the keys; with the tcgen05 pass one column by 64 tokens or all keys):
+ * 22 bits of what is down to 2^-17 of it, 11 down to 2^-28.  For bf16 inputs o is read out with the state,
+ * P and U (o = gam q S + P U) in 11 bits: within 2^-9.9 of the sum of its terms' magnitudes, beside its own
+ * rounding (2^-8 of o at most).  RECURRENT and mlstm_gdr_step read out in fp32, so AUTO's o changes by that
+ * much between 31 and 32 tokens.
+ * Infinities and NaN in v, S0, dout or dS stay in their value column of o, S_out, dv and dS0; inside a
+ * chunk they may reach tokens of the column before their own.
+ *
  *   V        a multiple of 8
  *   q, k     [B,HK,T,K]  dtype      required (if B, T > 0)
  *   v, o     [B,H,T,V]   dtype      required; o must not overlap an input
@@ -514,11 +528,13 @@ mlstm_status_t mlstm_step(const mlstm_step_params_t* p,
  * S[b], and pool >= B.  K a multiple of 8, at most 256; V a multiple of 8.
  *
  * mlstm_gdr_bwd: gradients of a loss given dout = dL/do [B,H,T,V] (dtype, strides p->o) and
- * dS = dL/dS_out [N,H,K,V] fp32 (NULL = 0).  dq, dk [B,HK,T,K] and dv [B,H,T,V] in the inputs' dtype
- * (each rounded once from fp32) by the strides s_dq, s_dk, s_dv; dg, dbeta [B,H,T] fp32 dense; dS0
- * [N,H,K,V] fp32.  All but dS0 (NULL = not written) are required if B, T > 0; gradients of q and k are
- * summed over the value heads that share them.  p->mode is ignored; K a multiple of 8, at most 128.
- * Sums have a fixed order: the same call gives the same bits.
+ * dS = dL/dS_out [N,H,K,V] fp32 (NULL = 0).  dq, dk [B,HK,T,K] and dv [B,H,T,V] in the inputs' dtype by the
+ * strides s_dq, s_dk, s_dv; dg, dbeta [B,H,T] fp32 dense; dS0 [N,H,K,V] fp32.  All but dS0 (NULL = not
+ * written) are required if B, T > 0; gradients of q and k are summed over the value heads that share them.
+ * p->mode is ignored; K a multiple of 8, at most 128.  Sums have a fixed order: the same call gives the same
+ * bits.  dv, dg, dbeta and dS0 have fp32's accuracy as above (dv rounded once from it); so have dq and dk for
+ * fp32 inputs.  For bf16 inputs the operands of their products have 11 bits: within 2^-9.3 of the sum of
+ * their terms' magnitudes, beside their rounding.
  */
 typedef enum { MLSTM_GDR_AUTO = 0, MLSTM_GDR_RECURRENT = 1, MLSTM_GDR_CHUNK = 2 } mlstm_gdr_mode_t;
 typedef struct {

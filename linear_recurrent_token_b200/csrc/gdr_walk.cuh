@@ -12,7 +12,9 @@ namespace gdr {
 // sequence, the final one) and by tile of 16 value columns.  Operands are fp16 tiles [16 values][tokens or
 // keys] with the pieces of a row permuted as in the other records, a tile's parts one behind the other;
 // each quarter of the tokens or keys has its scale.  NK: parts of an operand that only products rounded to
-// the output's type read, one (11 bits) for bf16, two for fp32.
+// the output's type read, one (11 bits) for bf16, two for fp32.  With one part dq and dk of bf16 inputs lie
+// 0.00168 and 0.00169 (relative, root of the mean square) from 64 bits, 0.00166 where only the result is
+// rounded; two would double what is kept, and of 128 keys only one block of columns would fit an SM.
 struct Kept {
   char* S;        // S at the chunk's start: [state][tile][2 parts][16][KP]
   float* S_inv;   // [state][tile][4]
@@ -332,7 +334,10 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
                                                                       const char* records, const Kept kept) {
   using L = Stage<T, KP, TN, GRAD>;
   constexpr int NP = L::NP, NK = kept_parts<T>(), KS = KP / 64;
-  constexpr bool FINE = L::P2;  // the output in fp32 accuracy: two parts of S, U and P under it
+  // The output in fp32 accuracy: two parts of S, U and P under it.  A bf16 output takes one, 11 bits under the 8 that
+  // it keeps: 0.00168 from 64 bits (relative, root of the mean square) instead of 0.00166, for 220 us instead of 244
+  // (16 heads of 128 x 128, 8192 tokens; 32 heads, 2048 tokens 85/94; 64 of 64 x 64 73/88).
+  constexpr bool FINE = L::P2;
   extern __shared__ __align__(128) char smem[];
   const int n = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the quarters' shares of the triangular products differ: over the tiles, each scheduler gets all of them
@@ -507,6 +512,9 @@ __global__ void __launch_bounds__(kWalkThreads<TN>, kWalkBlocks<T, KP, TN>) gdr_
 //   64 x 128 packed, 13 uneven sequences of 6007 tokens, 4 heads 77/94/105/120, 8: 101/114/114/123, 16: 163/170/176/161
 //   gradients 128 x 128, 16 heads 294/370/596, 64: 1100/848/797, 96: 1629/1249/1433, 128: 1965/1652/1560;
 //   64 x 64, 64 heads 422/437/558, 128: 819/858/724
+// fp32 inputs go by the same chains, which choose the faster of TN = 1 / 2 in all of these: 128 x 128, 16 heads
+// 117/174, 32: 231/196, 64: 439/373, 128: 782/727; 64 x 64, 32 heads 103/136, 64: 189/169, 128: 367/326;
+// gradients 128 x 128, 16 heads 382/547, 32: 741/650, 128: 2548/2481; 64 x 64, 32 heads 319/385, 64: 622/497
 inline double walk_cost(const GdrArgs& a, int TN) {
   const bool narrow = a.dtype == 1 && a.K <= 64, two = narrow && (TN == 1 || TN == 2);
   const int columns = TN ? 16 * TN : 128;

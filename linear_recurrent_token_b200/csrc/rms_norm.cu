@@ -43,8 +43,9 @@ __device__ __forceinline__ void load_vec(const T* p, float (&x)[VEC]) {
 
 // The rows ahead of the one in work, on their way from HBM: every thread copies its own vectors of NT tensors
 // into slots of shared memory that it alone reads, so that a wait for its own copies is all that a row costs
-// and some 100 KB an SM are in flight whatever the block does.  Odd widths (VEC 1) have no such copies and
-// read from memory.
+// and up to 100 KB an SM are in flight whatever the block does (less where a row leaves lanes or places empty: about
+// 18 KB for bf16 rows of 64 channels).  Odd widths (VEC 1), and fp32 rows of more than 8192 channels, have no such
+// copies and read from memory.
 template <typename T, int VEC, int NT, int TPR>
 struct Ring {
   static constexpr int NV = kElems / VEC, BLOCK = TPR > kThreads ? TPR : kThreads;

@@ -691,8 +691,9 @@ def gdr_fwd(q, k, v, g, beta, S0=None, *, seq_offsets=None, mode: str = "auto", 
     H a multiple of HK); g (log decay), beta [B,H,T] fp32; S0 [N,H,K,V] fp32 or None.  Tensors may be
     strided views with a contiguous last axis (a projection's [B,T,heads,width], transposed).
     seq_offsets [N+1] int32 packs N sequences into one batch row; tokens of no sequence stay as they are
-    in a given o and are zero in a new one.  mode "auto", "recurrent" or "chunk".  S_out may be S0.
-    Returns (o, S_out)."""
+    in a given o and are zero in a new one.  mode "auto", "recurrent" or "chunk" (include/mlstm.h: which
+    is taken, and how exact each is).  S_out may be S0.  workspace: a call's own unless given; give one to
+    ask gdr_status about the waits of the call.  Returns (o, S_out)."""
     sizes = _gdr_shapes(q, k, v, g, beta, seq_offsets)
     B, HK, H, T, K, V, N = sizes
     dev, states = q.device, (N, H, K, V)
@@ -753,8 +754,8 @@ def gdr_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None):
 def gdr_bwd(q, k, v, g, beta, do, S0=None, dS=None, *, seq_offsets=None, workspace=None, stream=None):
     """Gradients of the gated delta rule (mlstm_gdr_bwd): gdr_fwd's inputs, do [B,H,T,V] and dS
     [N,H,K,V] fp32 (the gradient of the final states) or None.  Returns a dict: dq, dk, dv in the inputs'
-    type, laid out like them where they fill their memory; dg, dbeta [B,H,T] and dS0 [N,H,K,V] fp32.
-    Gradients of tokens that no packed sequence holds are zero."""
+    type, laid out like them where they fill their memory; dg, dbeta [B,H,T] and dS0 [N,H,K,V] fp32.  How
+    exact each is: include/mlstm.h.  Gradients of tokens that no packed sequence holds are zero."""
     sizes = _gdr_shapes(q, k, v, g, beta, seq_offsets)
     B, HK, H, T, K, V, N = sizes
     dev, states = q.device, (N, H, K, V)
