@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gdr_tc_kernel(const GdrArgs a, 
         by_state(tm + kTmX, tm + kTmS + KP / 2, kd, false);
         by_state(tm + kTmX, tm + kTmS, kd, true);
         mma_commit(&bars.x_full);
-        by_state(tm + kTmO, tm + kTmS, qd, false);  // one part, as of P and U: 11 bits for an output of 8 (two: 172 -> 189 us)
+        by_state(tm + kTmO, tm + kTmS, qd, false);  // one part, as of P and U: 11 bits for an output of 8 (two: 175 -> 189 us)
       }
       __syncwarp();
       ok = wait(&bars.z_ready, c & 1);

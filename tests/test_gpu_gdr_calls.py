@@ -16,6 +16,13 @@ pytestmark = pytest.mark.gpu
 FAR = (1 << 32) + 64  # elements
 
 
+@pytest.fixture
+def give_back():
+    """What a test of 10 to 20 GB held goes back to the device."""
+    yield
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("mode", ["recurrent", "chunk"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("offsets", [(7, 77, 77, 140), (70, 71, 150), (128, 192)])
@@ -65,7 +72,7 @@ def far(x, buffer, at):
 
 
 @pytest.mark.parametrize("mode", ["recurrent", "chunk"])
-def test_strides_that_pass_32_bits(mode):
+def test_strides_that_pass_32_bits(mode, give_back):
     inp = inputs.gdr_inputs(1, 1, 2, 2, 64, 64, "bf16", seed=5)
     t = to_dev(inp, "bf16")
     a = [t[n] for n in ("q", "k", "v", "g", "beta", "S0")]
@@ -82,7 +89,7 @@ def test_strides_that_pass_32_bits(mode):
         assert all(torch.equal(want[n], got[n]) for n in want)
 
 
-def test_a_step_whose_rows_and_states_lie_far_apart():
+def test_a_step_whose_rows_and_states_lie_far_apart(give_back):
     """Batch strides of more than 2^32 elements, and a pool of more than 2^31."""
     inp = inputs.gdr_inputs(2, 1, 2, 1, 64, 64, "bf16", seed=6)
     t = to_dev(inp, "bf16")
@@ -148,7 +155,7 @@ def test_no_rows():
     assert torch.equal(S, before)
 
 
-def test_more_rows_than_32_bits_of_elements():
+def test_more_rows_than_32_bits_of_elements(give_back):
     """The norm and its gradients over 2^31 elements and a few rows more: the last rows as alone."""
     D = 4096
     rows = (1 << 31) // D + 3
